@@ -298,6 +298,128 @@ tr_status tr_topk(const float* scores, int64_t n, const int64_t* req_offsets, in
                   float* out_score, tr_stream stream);
 
 /*
+ * Generating candidates token by token (beam decoding over the user history).  One decode step
+ * of a batch of requests is: tr_prefix_attention in every layer, tr_beam_select over the
+ * vocabulary, tr_beam_reorder of the beams' own states.  Scratch is the caller's: none of these
+ * calls allocates or synchronises (the first one on a device sets up the status word, so make it
+ * before any stream capture), and a captured graph of them may be replayed beside other work as
+ * long as its buffers, the workspace among them, are its own.
+ */
+
+/*
+ * Attention of sequences that share their request's prefix.  Sequence s (a candidate or a beam)
+ * of request r has L_t query tokens; each attends to the request's prefix_len(r) prefix keys,
+ * stored once per request, and to the suffix_len[s] keys of the sequence's own suffix:
+ *     a_j = scale * q . k_j          over the prefix keys, then the suffix keys
+ *     lse = log sum_j exp(a_j)
+ *     out = sum_j exp(a_j - lse) v_j
+ * Query head h reads key/value head h / (n_head / n_kv_head).  A query token that sees no key
+ * gives out = 0 and lse = -inf.  Values behind a prefix or a suffix are never used (they may
+ * hold anything, NaN included).
+ */
+typedef struct {
+  int n_head, n_kv_head;      /* n_head a multiple of n_kv_head; n_head <= 1024                 */
+  int d_head;                 /* multiple of 8, <= 128                                          */
+  int L_t;                    /* query tokens per sequence, 1..TR_MAX_LT                        */
+  int causal;                 /* 0: every query token sees the whole suffix; 1: token t sees the
+                                 first suffix_len - (L_t - 1 - t) suffix keys (the query tokens
+                                 are the suffix's last L_t)                                     */
+  int suffix_cap;             /* tokens a suffix buffer holds per sequence; 0: no suffixes      */
+  float scale;                /* finite, usually 1 / sqrt(d_head)                               */
+  tr_dtype dtype;             /* of q, the keys, the values and out                             */
+  /* strides in elements; each a multiple of 16 bytes */
+  int64_t q_token;                            /* between query tokens (s, t), heads contiguous  */
+  int64_t prefix_token, prefix_head;          /* of k_prefix and of v_prefix                    */
+  int64_t suffix_seq, suffix_token, suffix_head; /* of k_suffix and of v_suffix                 */
+} tr_attn_desc;
+
+/* Bytes of workspace a tr_prefix_attention call with these arguments needs on the current
+ * device (0 is possible); SIZE_MAX when the arguments are invalid (tr_last_error() says why). */
+size_t tr_prefix_attention_workspace(const tr_attn_desc* desc, const int64_t* seq_offsets,
+                                     const int64_t* prefix_offsets, int R);
+
+/*
+ *   q              DEVICE [n][L_t][n_head][d_head], 16-byte aligned
+ *   seq_offsets    HOST int64 [R+1]: sequences of request r are seq_offsets[r] .. [r+1]-1;
+ *                  starts at 0, non-decreasing, ends at n (n * L_t < 2^31)
+ *   k_prefix, v_prefix  DEVICE [prefix_offsets[R]][n_kv_head][d_head], 16-byte aligned (may be
+ *                  NULL when there is no prefix token)
+ *   prefix_offsets HOST int64 [R+1]: prefix tokens of request r; starts at 0 or later (the
+ *                  tokens before belong to nobody), non-decreasing, below 2^31
+ *   k_suffix, v_suffix  DEVICE [n][suffix_cap][n_kv_head][d_head], 16-byte aligned (NULL when
+ *                  suffix_cap = 0)
+ *   suffix_len     DEVICE int32 [n]; a length outside 0..suffix_cap is clamped to it and sets
+ *                  the device status word (TR_ERR_KEY_RANGE via tr_sync_status)
+ *   out            DEVICE [n][L_t][n_head][d_head], contiguous, 16-byte aligned
+ *   lse            DEVICE fp32 [n][L_t][n_head], contiguous, or NULL
+ *   workspace      DEVICE, 16-byte aligned, at least tr_prefix_attention_workspace() bytes, the
+ *                  call's own until it has run
+ * 1 <= R <= TR_MAX_REQUESTS.  TR_BF16 rounds the softmax numerators of a value product to bf16
+ * (its tensor-core operand) and computes everything else in fp32; TR_F32 computes in fp32
+ * throughout.  The result does not depend on which other requests share the call by more than
+ * the rounding of the fp32 sums: the split of a long prefix over SMs goes by the whole batch.
+ */
+tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q, const int64_t* seq_offsets,
+                              const void* k_prefix, const void* v_prefix, const int64_t* prefix_offsets,
+                              const void* k_suffix, const void* v_suffix, const int32_t* suffix_len, int R,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes, tr_stream stream);
+
+/*
+ * Beam selection: the k best continuations of every request over its W beams and the vocabulary.
+ *     total(b, v) = cum[b] + logits[b][v] - log sum_u exp(logits[b][u])
+ * Best first.  Totals are compared in 64 bits; equal totals go by lower beam, then higher logit,
+ * then lower token.
+ *   logits     DEVICE [R*W][V] of logits_dtype, `ld` elements from row to row (rows at 16-byte
+ *              aligned addresses are read fastest)
+ *   cum        DEVICE fp32 [R*W]: a beam's log probability so far; a beam whose value is not
+ *              finite is dead and offers nothing (the logits of dead and of finished beams are
+ *              not read)
+ *   finished   DEVICE uint8 [R*W] or NULL: a finished beam (non-zero) offers one continuation,
+ *              pad_token with the unchanged total cum[b]
+ *   allowed    DEVICE uint32 [R*W][allowed_ld] or NULL: token v may follow beam b when bit v % 32
+ *              of word v / 32 is set (a trie of valid items).  The normalisation stays over the
+ *              whole vocabulary; finished beams are not masked
+ *   parent, token  DEVICE int32 [R][k]: beam within the request, token; -1, -1 where fewer than
+ *              k continuations have a total above -inf
+ *   score      DEVICE fp32 [R][k]: the total (padding -inf)
+ * A NaN logit counts as -inf; a row with +inf logits gives its whole probability to them in
+ * equal parts; a row of -inf offers nothing.  1 <= W <= TR_MAX_BEAMS, 1 <= k <= TR_MAX_BEAM_K,
+ * 1 <= V <= 2^24, 0 <= pad_token < 2^24, R * W < 2^20.  The result depends on nothing but the
+ * request's own rows.  workspace: DEVICE, 16-byte aligned, tr_beam_select_workspace() bytes, the
+ * call's own until it has run (SIZE_MAX: invalid sizes, tr_last_error() says why).
+ */
+#define TR_MAX_BEAMS 256
+#define TR_MAX_BEAM_K 256
+size_t tr_beam_select_workspace(int R, int W, int V, int k);
+tr_status tr_beam_select(const void* logits, tr_dtype logits_dtype, int64_t ld, const float* cum,
+                         const uint8_t* finished, const uint32_t* allowed, int64_t allowed_ld, int R, int W, int V,
+                         int k, int pad_token, int32_t* parent, int32_t* token, float* score, void* workspace,
+                         size_t workspace_bytes, tr_stream stream);
+
+/*
+ * Moves the states of surviving beams to their new places: for every state
+ *     dst row r*W_out + i  =  src row r*W_in + parent[r*W_out + i]
+ * A negative parent leaves its dst row as it was; one >= W_in does too and sets the device
+ * status word (TR_ERR_KEY_RANGE).  dst == src reorders in place (then W_in == W_out and the row
+ * strides are equal); a dst that shares bytes with any other src or dst of the call is refused
+ * (rows interleaved at one stride, like the K and V of a joint cache, share none).
+ *   states  HOST array [n_states] (<= TR_MAX_STATES); any dtype: rows are row_bytes bytes
+ *   parent  DEVICE int32 [R][W_out]
+ * 1 <= W_in, W_out <= TR_MAX_BEAMS, R * W < 2^20.  When every address, stride and row_bytes of
+ * the call is a multiple of 16, rows are moved 16 bytes at a time; else 4 bytes, or one byte.
+ */
+#define TR_MAX_STATES 64
+typedef struct {
+  void* dst;            /* DEVICE [R*W_out] rows                                  */
+  const void* src;      /* DEVICE [R*W_in] rows                                   */
+  int64_t dst_stride;   /* bytes from row to row, >= row_bytes                    */
+  int64_t src_stride;
+  int64_t row_bytes;    /* bytes of a row to move (for a cache, its filled part)  */
+} tr_beam_state;
+tr_status tr_beam_reorder(const tr_beam_state* states, int n_states, const int32_t* parent, int R, int W_in,
+                          int W_out, tr_stream stream);
+
+/*
  * No-allocation variant of tr_prefill_user.  The paper has no counterpart: this entry point
  * exists for callers that cannot call cudaMalloc when the user side runs -- code running
  * while a CUDA stream capture is open (allocation is not a capturable operation), serving

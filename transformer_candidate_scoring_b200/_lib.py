@@ -13,6 +13,7 @@ TR_MAX_TABLES, TR_MAX_REQUESTS, TR_MAX_LU = 64, 64, 256
 TR_NOALLOC_SCRATCH_BYTES = 1 << 20
 TR_MAX_TOPK = 4096
 TR_MAX_LT = 16
+TR_MAX_BEAMS, TR_MAX_BEAM_K, TR_MAX_STATES = 256, 256, 64
 
 _fp = C.POINTER(C.c_float)
 
@@ -36,6 +37,18 @@ class ModelWeights(C.Structure):
 
 class Table(C.Structure):
     _fields_ = [("data", C.c_void_p), ("n_rows", C.c_int64), ("dtype", C.c_int)]
+
+
+class AttnDesc(C.Structure):
+    _fields_ = [("n_head", C.c_int), ("n_kv_head", C.c_int), ("d_head", C.c_int), ("L_t", C.c_int),
+                ("causal", C.c_int), ("suffix_cap", C.c_int), ("scale", C.c_float), ("dtype", C.c_int),
+                ("q_token", C.c_int64), ("prefix_token", C.c_int64), ("prefix_head", C.c_int64),
+                ("suffix_seq", C.c_int64), ("suffix_token", C.c_int64), ("suffix_head", C.c_int64)]
+
+
+class BeamState(C.Structure):
+    _fields_ = [("dst", C.c_void_p), ("src", C.c_void_p), ("dst_stride", C.c_int64), ("src_stride", C.c_int64),
+                ("row_bytes", C.c_int64)]
 
 
 SIGNATURES = {
@@ -63,6 +76,16 @@ SIGNATURES = {
                                                    C.c_int, C.c_void_p, C.c_void_p]),
     "tr_topk": (C.c_int, [C.c_void_p, C.c_int64, C.POINTER(C.c_int64), C.c_int, C.c_int, C.c_void_p, C.c_void_p,
                           C.c_void_p]),
+    "tr_prefix_attention_workspace": (C.c_size_t, [C.POINTER(AttnDesc), C.POINTER(C.c_int64), C.POINTER(C.c_int64),
+                                                   C.c_int]),
+    "tr_prefix_attention": (C.c_int, [C.POINTER(AttnDesc), C.c_void_p, C.POINTER(C.c_int64), C.c_void_p, C.c_void_p,
+                                      C.POINTER(C.c_int64), C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p,
+                                      C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tr_beam_select_workspace": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
+    "tr_beam_select": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int,
+                                 C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                 C.c_size_t, C.c_void_p]),
+    "tr_beam_reorder": (C.c_int, [C.POINTER(BeamState), C.c_int, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p]),
     "tr_sync_status": (C.c_int, [C.c_void_p, C.c_int]),
 }
 
