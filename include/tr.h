@@ -325,9 +325,9 @@ typedef struct {
                                  first suffix_len - (L_t - 1 - t) suffix keys (the query tokens
                                  are the suffix's last L_t)                                     */
   int suffix_cap;             /* tokens a suffix buffer holds per sequence; 0: no suffixes      */
-  float scale;                /* finite, usually 1 / sqrt(d_head)                               */
+  float scale;                /* positive, usually 1 / sqrt(d_head)                             */
   tr_dtype dtype;             /* of q, the keys, the values and out                             */
-  /* strides in elements; each a multiple of 16 bytes */
+  /* strides in elements; each positive and a multiple of 16 bytes (suffixes: when there are any) */
   int64_t q_token;                            /* between query tokens (s, t), heads contiguous  */
   int64_t prefix_token, prefix_head;          /* of k_prefix and of v_prefix                    */
   int64_t suffix_seq, suffix_token, suffix_head; /* of k_suffix and of v_suffix                 */

@@ -38,7 +38,7 @@ def attn(lib, d=None, seq=(0, 2, 3), pre=(0, 5, 9), R=2, q=P, kp=P, vp=P, ks=P, 
 
 BAD_DESC = [dict(n_head=7), dict(n_kv_head=0), dict(n_head=0), dict(n_head=1026, n_kv_head=2), dict(d_head=60), dict(d_head=0),
             dict(d_head=136), dict(L_t=0), dict(L_t=17), dict(causal=2), dict(suffix_cap=-1), dict(scale=float("nan")),
-            dict(scale=float("inf")), dict(dtype=5), dict(q_token=516), dict(prefix_token=-128), dict(prefix_head=4),
+            dict(scale=float("inf")), dict(scale=0.0), dict(scale=-1.0), dict(prefix_token=0), dict(dtype=5), dict(q_token=516), dict(prefix_token=-128), dict(prefix_head=4),
             dict(suffix_seq=1), dict(suffix_token=2), dict(suffix_head=12), dict(q_token=1 << 40)]
 
 

@@ -297,7 +297,11 @@ def _kv_strides(k, v, what: str):
         raise ValueError(f"{what}: keys and values differ in strides")
     if k.numel() > 0 and k.shape[-1] > 1 and k.stride(-1) != 1:
         raise ValueError(f"{what}: the head dimension must be contiguous")
-    return k.stride()
+    # a dimension of one entry may come with any stride; it is never multiplied
+    inner, strides = k.shape[-1], []
+    for size, stride in zip(reversed(k.shape[:-1]), reversed(k.stride()[:-1])):
+        strides.insert(0, stride if size > 1 else max(inner, 1))
+    return strides
 
 
 def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, prefix_offsets: Sequence[int],
@@ -338,7 +342,7 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
         raise ValueError("prefix_offsets and seq_offsets differ in length")
     if so_list[-1] != n or po_list[-1] > k_prefix.shape[0]:
         raise ValueError("seq_offsets must end at n, prefix_offsets within k_prefix")
-    S, sk = 0, (0, 0, 0, 0)
+    S, sk = 0, (0, 0, 0)
     if k_suffix is not None:
         if v_suffix is None or suffix_len is None:
             raise ValueError("k_suffix, v_suffix and suffix_len come together")

@@ -1,0 +1,542 @@
+// The prefix part of tr_prefix_attention on the tensor cores (bf16).
+//
+// A request's query rows of one key head -- sequences x query tokens x the heads that share the
+// key head -- form one matrix Q against the shared keys, so the prefix is an attention of many
+// rows over one K and V:  S = Q K^T (128 rows x 128 keys per step, TMEM), P = 2^(c S - c m) in
+// registers with the running row maximum m and sum l, O += P V (P back in TMEM as bf16, the A
+// operand; O in TMEM, fp32).  Nothing of S or P leaves the SM.
+//
+// A CTA holds two row tiles, each with its own softmax warpgroup, so that the tensor core works
+// on one tile while the other is in its exponentials.  A unit of more than 128 rows gives the
+// two tiles different rows of the same keys; a unit of at most 128 rows gives both the same rows
+// and every other step of keys (their results are merged at the unit's end).
+//
+//   TMEM, 512 columns   S/P of tile 0, S/P of tile 1 (128 each), O of tile 0, O of tile 1
+//   shared memory       Q of both tiles, a ring of K steps and one of V steps; all in the
+//                       128-byte-swizzled layout (K-major for Q and K; V is [keys][d_head], the
+//                       MN-major form), K and V by TMA, d_head padded to 64 or 128 by TMA's zeros
+//   warps 0-3, 4-7      softmax of tile 0 and 1, one row per thread, and the epilogue
+//   warps 8, 9, 10      K loads, V loads, MMA issue; warp 11 owns the tensor memory
+//
+// The row maximum that O and l are relative to is raised only when the new one is more than 2^8
+// away (then O is rescaled in TMEM): numerators stay below 2^8 and sums in fp32 range.  Values
+// behind a prefix are kept out twice: their scores are replaced by -inf, and the V rows that the
+// last 16-key slice would still multiply by 0 are zeroed in shared memory (0 x NaN is NaN).
+//
+// Every wait is bounded: a stalled barrier sets an error bit and the kernel unwinds.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "prefix_attention.cuh"
+#include "tc_common.cuh"
+
+namespace tr {
+namespace attn {
+namespace {
+
+using namespace tc;
+
+constexpr int kM = 128, kN = kStepKeys;
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168, kCtlRegs = 56, kSoftmaxRegs = 216;
+static_assert(128 * kCtlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536,
+              "register split");
+constexpr float kRaise = 8.f;    // log2 of how far numerators may exceed 1
+
+template <int DH>    // d_head padded to 64 or 128
+struct Smem {
+  static constexpr int TILE = 128 * DH * 2;
+  static constexpr int NK = DH == 128 ? 3 : 4, NV = DH == 128 ? 2 : 4;
+  static constexpr int Q = 0, K = 2 * TILE, V = K + NK * TILE, BAR = V + NV * TILE;
+  static constexpr int ML = BAR + 256;           // m and l of tile 1's rows (merge)
+  static constexpr int BYTES = ML + 1024 + 1024;   // + alignment of the base
+};
+static_assert(Smem<128>::BYTES <= 232448 && Smem<64>::BYTES <= 232448, "shared memory plan");
+
+struct TcParams {
+  CUtensorMap kmap, vmap;
+  AttnParams a;
+  bool direct;
+};
+
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {    // K-major, 128-byte swizzle
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// MN-major, 128-byte swizzle: 64 elements of N per 128-byte row, 8 K rows per 1024-byte atom;
+// the next 64 of N `n_step` bytes further, the next 8 of K 1024 bytes further.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t n_step) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)((n_step >> 4) & 0x3FFF) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+constexpr uint32_t kBMajorMN = 1u << 16;
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  tmem_ld16(taddr, v);
+  tmem_ld16(taddr + 16, v + 16);
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A warp's wait; every lane gives up when one does.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+
+struct Bars {
+  uint32_t kfull, kempty, vfull, vempty;   // rings, 8 bytes apart
+  uint32_t qfull, sfull, pfull, odone;     // per tile
+  uint32_t ml_full, ml_empty;
+};
+
+struct Unit {
+  int r, hk, m0, rows, split;
+  int tok, keys;       // first key token, keys of this chunk
+  int steps;
+  bool two;            // the two tiles hold different rows
+  __device__ int jobs(int t) const { return two ? steps : (steps + 1 - t) / 2; }
+  __device__ int step_of(int t, int k) const { return two ? k : 2 * k + t; }   // step of tile t's k-th job
+};
+
+__device__ __forceinline__ Unit unit_at(const AttnParams& p, int u) {
+  int lo = 0, hi = p.R - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.req[mid].first_unit <= u) lo = mid; else hi = mid - 1;
+  }
+  const RequestPlan& q = p.req[lo];
+  const int m_all = (q.s1 - q.s0) * p.d.L_t * (p.d.n_head / p.d.n_kv_head);
+  const int n_m = (m_all + kUnitRows - 1) / kUnitRows;
+  int i = u - q.first_unit;
+  Unit x;
+  x.r = lo;
+  x.m0 = (i % n_m) * kUnitRows;      // units that share keys are neighbours
+  i /= n_m;
+  x.split = i % q.n_split;
+  x.hk = i / q.n_split;
+  x.rows = min(kUnitRows, m_all - x.m0);
+  x.two = x.rows > kM;
+  const int k0 = x.split * q.chunk * kN;
+  x.tok = q.p0 + k0;
+  x.keys = min(q.chunk * kN, q.p1 - x.tok);
+  x.steps = (x.keys + kN - 1) / kN;
+  return x;
+}
+
+// One thread: streams the K (or V) steps of every unit into its ring.
+template <int DH>
+__device__ void load_steps(const AttnParams& p, const CUtensorMap* map, uint32_t ring, int slots, uint32_t full, uint32_t empty,
+                           volatile int* abort_flag) {
+  int s = 0;
+  uint32_t ph = 0;
+  bool ok = true;
+  uint32_t pending = 0, par = 0;           // bit s: a load of slot s was issued, and its parity
+  for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
+    const Unit x = unit_at(p, u);
+    for (int j = 0; j < x.steps; ++j) {
+      if (!(ok = mbar_wait_idle(empty + 8 * s, ph ^ 1, abort_flag))) break;
+      const uint32_t dst = ring + s * Smem<DH>::TILE;
+      mbar_arrive_expect_tx(full + 8 * s, Smem<DH>::TILE);
+#pragma unroll
+      for (int h = 0; h < DH / 64; ++h) tma_load_3d(dst + h * (128 * 128), map, h * 64, x.hk, x.tok + j * kN, full + 8 * s);
+      pending |= 1u << s;
+      par = (par & ~(1u << s)) | (ph << s);
+      if (++s == slots) { s = 0; ph ^= 1; }
+    }
+  }
+  if (!ok) {   // unwinding: let the copies in flight land before the CTA's memory is given back
+    int none = 0;
+    for (int i = 0; i < slots; ++i)
+      if (pending >> i & 1) mbar_wait_idle(full + 8 * i, par >> i & 1, &none, 200000000ull);
+  }
+}
+
+// The whole warp: lane 0 issues, all lanes zero V rows behind the prefix.
+template <int DH>
+__device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, const Bars& b, int lane, volatile int* abort_flag) {
+  using L = Smem<DH>;
+  const int dk = (p.a.d.d_head + 15) / 16;                 // 16-wide slices of d_head
+  const uint32_t id_o = idesc_bf16(kM, dk * 16) | kBMajorMN;
+  int ks = 0, vs = 0;                                      // ring slots of the current step
+  uint32_t kph = 0, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+  bool ok = true;
+  for (int u = blockIdx.x; u < p.a.n_units && ok; u += gridDim.x) {
+    const Unit x = unit_at(p.a, u);
+    const int n_jobs = x.two ? 2 * x.steps : x.steps;
+    auto qk = [&](int i) {
+      const int t = i & 1, step = x.two ? i >> 1 : i;
+      if (i < 2) {
+        ok = ok && wait_all(b.qfull + 8 * t, qph[t], abort_flag);
+        qph[t] ^= 1;
+      }
+      ok = ok && wait_all(b.kfull + 8 * ks, kph, abort_flag);
+      if (!ok) return;
+      const int n = (min(kN, x.keys - step * kN) + 15) & ~15;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t qa = smem + L::Q + t * L::TILE, ka = smem + L::K + ks * L::TILE, id = idesc_bf16(kM, n);
+        for (int kk = 0; kk < dk; ++kk) {
+          const uint32_t o = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+          mma_bf16(tmem + t * kN, desc_k(qa + o), desc_k(ka + o), id, kk > 0);
+        }
+        mma_commit(b.sfull + 8 * t);
+        if (!x.two || t == 1) mma_commit(b.kempty + 8 * ks);
+      }
+      if (!x.two || t == 1)
+        if (++ks == L::NK) { ks = 0; kph ^= 1; }
+    };
+    qk(0);
+    if (n_jobs > 1) qk(1);
+    for (int i = 0; i < n_jobs && ok; ++i) {
+      const int t = i & 1, k = i >> 1, step = x.two ? k : i;
+      const int valid = min(kN, x.keys - step * kN);
+      ok = wait_all(b.vfull + 8 * vs, vph, abort_flag);
+      const uint32_t va = smem + L::V + vs * L::TILE;
+      if (ok && (valid & 15) && (t == 0 || !x.two)) {
+        // rows valid .. the end of their 16-key slice: 16-byte pieces of the 128-byte rows
+        const int n_rows = 16 - (valid & 15);
+        for (int c = lane; c < n_rows * 8 * (DH / 64); c += 32) {
+          const int h = c / (n_rows * 8), rr = (c / 8) % n_rows;
+          st_shared_v4(va + h * (128 * 128) + (valid + rr) * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      ok = ok && wait_all(b.pfull + 8 * t, pph[t], abort_flag);
+      pph[t] ^= 1;
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const int nk = (valid + 15) / 16;
+        for (int kk = 0; kk < nk; ++kk)
+          mma_bf16_ta(tmem + 2 * kN + t * 128, tmem + t * kN + kk * 8, desc_mn(va + kk * 2048, 128 * 128), id_o,
+                      (k > 0 || kk > 0) ? 1u : 0u);
+        if (!x.two || t == 1) mma_commit(b.vempty + 8 * vs);
+        if (i + 2 >= n_jobs) mma_commit(b.odone + 8 * t);
+      }
+      if (!x.two || t == 1)
+        if (++vs == L::NV) { vs = 0; vph ^= 1; }
+      if (i + 2 < n_jobs) qk(i + 2);
+    }
+  }
+}
+
+// A softmax warpgroup (tile t): loads its Q rows, turns S into P step by step, writes the result.
+template <int DH>
+__device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t smem, float* sml, const Bars& b,
+                             volatile int* abort_flag) {
+  using L = Smem<DH>;
+  const AttnParams& p = tp.a;
+  const int tid = threadIdx.x & 127, lane = tid & 31, wrow = tid & ~31;    // wrow: the warp's first row
+  const uint32_t lanes = (uint32_t)wrow << 16;                              // its TMEM lanes
+  const uint32_t s_addr = tmem + t * kN + lanes, o_addr = tmem + 2 * kN + t * 128 + lanes;
+  const int D = p.d.d_head, G = p.d.n_head / p.d.n_kv_head;
+  const float c = p.d.scale * kLog2e;
+  const uint64_t c2 = f32x2(c, c);
+  uint32_t sph = 0, oph = 0, xph = 0;
+  bool ok = true;
+  for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
+    const Unit x = unit_at(p, u);
+    const RequestPlan& rq = p.req[x.r];
+    const int base = x.two ? t * kM : 0;
+    const bool live = base + tid < x.rows, warp_live = base + wrow < x.rows;
+    const int m = x.m0 + base + tid;                         // row within (request, key head)
+    const int64_t token = (int64_t)rq.s0 * p.d.L_t + m / G;  // query token of the batch
+    const int head = x.hk * G + m % G;
+    const int jobs = x.jobs(t);
+    if (jobs > 0) {
+      // ---- Q rows (the previous unit's products have read them: its last S was seen)
+      const uint32_t row = smem + L::Q + t * L::TILE + tid * 128;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + token * p.d.q_token + (int64_t)head * D);
+      const int chunks = D / 8, pad = ((D + 15) / 16) * 2;
+#pragma unroll 4
+      for (int i = 0; i < pad; ++i) {
+        const uint4 v = live && i < chunks ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+        st_shared_v4(row + (i >> 3) * (128 * 128) + (((i & 7) ^ (tid & 7)) << 4), v.x, v.y, v.z, v.w);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(b.qfull + 8 * t);
+    }
+    float mx = -INFINITY;          // the reference maximum of S, unscaled
+    float l = 0.f;
+    for (int k = 0; k < jobs; ++k) {
+      const int valid = min(kN, x.keys - x.step_of(t, k) * kN);
+      if (!(ok = wait_all(b.sfull + 8 * t, sph, abort_flag))) break;
+      sph ^= 1;
+      tc_fence_after();
+      if (warp_live) {
+        float s[kN];
+#pragma unroll
+        for (int i = 0; i < kN / 32; ++i)
+          if (i * 32 < valid) tmem_ld32(s_addr + 32 * i, s + 32 * i);
+        tmem_wait_ld();
+        reg_fence<kN>(s);
+        if (valid < kN) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
+            if (i >= valid) s[i] = -INFINITY;
+        }
+        float n0 = mx, n1 = s[0], n2 = s[1], n3 = s[2];
+#pragma unroll
+        for (int i = 3; i + 7 < kN; i += 8) {
+          n0 = max3(n0, s[i], s[i + 1]);
+          n1 = max3(n1, s[i + 2], s[i + 3]);
+          n2 = max3(n2, s[i + 4], s[i + 5]);
+          n3 = max3(n3, s[i + 6], s[i + 7]);
+        }
+        n0 = max3(n0, s[123], s[124]);
+        n1 = max3(n1, s[125], s[126]);
+        const float nm = max3(fmaxf(n0, s[127]), n1, fmaxf(n2, n3));
+        const bool raise = k == 0 || (nm - mx) * c > kRaise;
+        if (__any_sync(0xffffffffu, raise)) {
+          // (the first step has no O yet; S of this step was committed after the last P V)
+          const float f = raise ? (nm == mx ? 1.f : ex2((mx - nm) * c)) : 1.f;
+          if (raise) mx = nm;
+          if (k > 0) {
+            l *= f;
+            for (int i = 0; i * 16 < D; ++i) {
+              float o[16];
+              tmem_ld16(o_addr + 16 * i, o);
+              tmem_wait_ld();
+              reg_fence<16>(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tmem_st16(o_addr + 16 * i, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float mc = mx == -INFINITY ? 0.f : mx * c;      // keys of -inf weigh nothing, NaN stays NaN
+        const uint64_t mc2 = f32x2(-mc, -mc);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < kN / 32; ++i)
+          if (i * 32 < valid) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a, bb;
+              f32x2_split(fma_f32x2(f32x2(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), c2, mc2), a, bb);
+              a = ex2(a);
+              bb = ex2(bb);
+              sum[e & 1] = add_f32x2(sum[e & 1], f32x2(a, bb));
+              w[e] = pack_bf16(a, bb);
+            }
+            asm volatile(
+                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                    s_addr + 16 * i),
+                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
+                "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+                : "memory");
+          }
+        float a0, a1;
+        f32x2_split(add_f32x2(sum[0], sum[1]), a0, a1);
+        l += a0 + a1;
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b.pfull + 8 * t);
+    }
+    if (!ok) break;
+    // ---- the result of the unit's rows
+    if (jobs > 0) {
+      if (!(ok = wait_all(b.odone + 8 * t, oph, abort_flag))) break;
+      oph ^= 1;
+    }
+    float w0 = 1.f, w1 = 0.f, lsum = l, mref = mx;
+    if (!x.two) {
+      // both tiles hold these rows: tile 1 hands its maximum and sum over, tile 0 reads its O
+      if (t == 1) {
+        sml[tid] = jobs > 0 ? mx : -INFINITY;
+        sml[128 + tid] = l;
+        tc_fence_before();
+        mbar_arrive(b.ml_full);
+        ok = wait_all(b.ml_empty, xph, abort_flag);
+        xph ^= 1;
+        continue;
+      }
+      if (!(ok = wait_all(b.ml_full, xph, abort_flag))) break;
+      xph ^= 1;
+      const float m1 = sml[tid], l1 = sml[128 + tid];
+      mref = fmaxf(mx, m1);
+      const float mb = mref == -INFINITY ? 0.f : mref;
+      w0 = mx == mref ? 1.f : ex2((mx - mb) * c);
+      w1 = m1 == mref ? 1.f : ex2((m1 - mb) * c);
+      lsum = w0 * l + w1 * l1;
+    }
+    tc_fence_after();
+    const bool second = !x.two && x.steps > 1;               // tile 1 has an O
+    if (warp_live) {
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+      const float lse2 = lsum == 0.f ? -INFINITY : __fmul_rn(mref, c) + log2f(lsum);
+      const int64_t row = token * p.d.n_head + head;
+      const int64_t part = rq.part + x.split * request_rows(p, x.r) + (row - (int64_t)rq.s0 * p.d.L_t * p.d.n_head);
+      for (int i = 0; i * 16 < D; ++i) {
+        float o[16], o1[16];
+        tmem_ld16(o_addr + 16 * i, o);
+        if (second) tmem_ld16(o_addr + 128 + 16 * i, o1);
+        tmem_wait_ld();
+        reg_fence<16>(o);
+        reg_fence<16>(o1);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = (second ? o[e] * w0 + o1[e] * w1 : o[e] * w0) * inv;
+        if (live) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (16 * i + 8 * h < D) {
+              if (tp.direct) {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D + 16 * i + 8 * h) =
+                    make_uint4(pack_bf16(o[8 * h], o[8 * h + 1]), pack_bf16(o[8 * h + 2], o[8 * h + 3]),
+                               pack_bf16(o[8 * h + 4], o[8 * h + 5]), pack_bf16(o[8 * h + 6], o[8 * h + 7]));
+              } else {
+                float4* d = reinterpret_cast<float4*>(p.part_o + part * D + 16 * i + 8 * h);
+                d[0] = make_float4(o[8 * h], o[8 * h + 1], o[8 * h + 2], o[8 * h + 3]);
+                d[1] = make_float4(o[8 * h + 4], o[8 * h + 5], o[8 * h + 6], o[8 * h + 7]);
+              }
+            }
+        }
+      }
+      if (live) {
+        if (!tp.direct)
+          p.part_lse[part] = lse2;
+        else if (p.lse)
+          p.lse[row] = lse2 * kLn2;
+      }
+    }
+    tc_fence_before();
+    if (!x.two) mbar_arrive(b.ml_empty);
+  }
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ TcParams p) {
+  using L = Smem<DH>;
+  extern __shared__ uint8_t raw[];
+  const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* gbase = raw + (smem - smem_u32(raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Bars b;
+  uint32_t at = smem + L::BAR;
+  auto take = [&](int n) { const uint32_t r = at; at += 8 * n; return r; };
+  b.kfull = take(L::NK); b.kempty = take(L::NK); b.vfull = take(L::NV); b.vempty = take(L::NV);
+  b.qfull = take(2); b.sfull = take(2); b.pfull = take(2); b.odone = take(2);
+  b.ml_full = take(1); b.ml_empty = take(1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::BAR + 248);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::BAR + 252);
+  static_assert((2 * L::NK + 2 * L::NV + 10) * 8 <= 248, "barriers");
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < L::NK; ++i) { mbar_init(b.kfull + 8 * i, 1); mbar_init(b.kempty + 8 * i, 1); }
+    for (int i = 0; i < L::NV; ++i) { mbar_init(b.vfull + 8 * i, 1); mbar_init(b.vempty + 8 * i, 1); }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(b.qfull + 8 * t, 128);
+      mbar_init(b.sfull + 8 * t, 1);
+      mbar_init(b.pfull + 8 * t, 4);
+      mbar_init(b.odone + 8 * t, 1);
+    }
+    mbar_init(b.ml_full, 128);
+    mbar_init(b.ml_empty, 128);
+    mbar_fence_init();
+  }
+  if (warp == 11) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
+    if (warp == 8 && lane == 0) load_steps<DH>(p.a, &p.kmap, smem + L::K, L::NK, b.kfull, b.kempty, abort_flag);
+    if (warp == 9 && lane == 0) load_steps<DH>(p.a, &p.vmap, smem + L::V, L::NV, b.vfull, b.vempty, abort_flag);
+    if (warp == 10) issue_mmas<DH>(p, tmem, smem, b, lane, abort_flag);
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    softmax_tile<DH>(p, warp >> 2, tmem, smem, reinterpret_cast<float*>(gbase + L::ML), b, abort_flag);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 11) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.a.status, STATUS_KERNEL_TIMEOUT);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// [tokens][key heads][d_head] with the caller's strides; boxes of 128 tokens x 64 columns of one
+// head, columns past d_head and tokens past the end read as zeros.
+tr_status encode_map(CUtensorMap* map, const void* base, const AttnParams& p) {
+  auto encode = get_encode();
+  if (!encode) return fail(TR_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const int64_t row = p.d.d_head;
+  // a dimension of one entry may come with any stride: it is never multiplied
+  const int64_t hs = p.d.n_kv_head > 1 ? p.d.prefix_head : row, ts = p.req[p.R].p0 > 1 ? p.d.prefix_token : row;
+  cuuint64_t gdim[3] = {(cuuint64_t)row, (cuuint64_t)p.d.n_kv_head, (cuuint64_t)p.req[p.R].p0};
+  cuuint64_t gstride[2] = {(cuuint64_t)hs * 2, (cuuint64_t)ts * 2};
+  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t estride[3] = {1, 1, 1};
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estride,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TR_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return TR_OK;
+}
+
+template <int DH>
+tr_status launch(const TcParams& p, int sms, cudaStream_t st) {
+  TR_TRY(ensure_smem_attr((const void*)prefix_kernel<DH>, Smem<DH>::BYTES));
+  prefix_kernel<DH><<<std::min(p.a.n_units, sms), kThreads, Smem<DH>::BYTES, st>>>(p);
+  TR_LAUNCH_CHECK("prefix_kernel");
+  return TR_OK;
+}
+
+}  // namespace
+
+tr_status launch_prefix_tc(const AttnParams& a, bool direct, cudaStream_t st) {
+  TcParams p;
+  memset(&p, 0, sizeof p);
+  p.a = a;
+  p.direct = direct;
+  TR_TRY(encode_map(&p.kmap, a.k_prefix, a));
+  TR_TRY(encode_map(&p.vmap, a.v_prefix, a));
+  int dev = 0, sms = 0;
+  TR_CUDA_TRY(cudaGetDevice(&dev));
+  TR_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  return a.d.d_head <= 64 ? launch<64>(p, sms, st) : launch<128>(p, sms, st);
+}
+
+}  // namespace attn
+}  // namespace tr
