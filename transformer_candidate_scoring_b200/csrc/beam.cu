@@ -3,19 +3,19 @@
 // Selection.  total(b, v) = cum[b] + x[b][v] - log sum_u exp(x[b][u]); the k best (b, v) of each
 // request.  The logits are the traffic (2 or 4 bytes per (b, v), read once); the results are a
 // few KB.  Two launches:
-//   beam_chunk_kernel  one CTA per (row, chunk of 256 threads x 8 16-byte vectors), the chunk
-//     held in registers between its uses: the running maximum and the sum of exponentials of
-//     the chunk, and the chunk's candidates -- every logit that reaches a threshold below which
-//     no chunk element can be among the k best.  The threshold is the k-th largest of the 256
-//     threads' own maxima (at least k elements reach it, and for a vocabulary in no particular
-//     order not many more than k do), found by bisection with one block-wide count per step.
-//   beam_merge_kernel  one CTA per request: the rows' log-sum-exp from the chunks' sums (in 64
-//     bits: two beams' totals are compared across rows), the same threshold step over all
-//     candidates' totals, then a sort of the few that remain.
-// When more elements reach a threshold than its buffer holds (long runs of equal logits), the
-// exact k-th key is found by bisection over the elements themselves.
+//   beam_sum_kernel   one warp per tile of 32 lanes x 8 16-byte vectors of a row, held in
+//     registers: the tile's maximum and sum of exponentials, and each lane's best logit (of its
+//     "group" of 64 bf16 or 32 fp32 tokens) -- nothing else, no shared memory and no barrier, so
+//     that the loads of the next warps are always in flight.
+//   beam_pick_kernel  one CTA per request: the rows' log-sum-exp (in 64 bits: two beams' totals
+//     are compared across rows), the tiles' best totals, a bound that at least k tiles reach (or
+//     groups, of few tiles; the k-th largest of the threads' own best, by bisection with one
+//     block-wide count per step), and then only the tiles, groups and logits that reach it --
+//     about k of each -- are looked at, the tokens among them cut down the same way and ranked.
+// When more tokens reach the bound than the sort holds (long runs of equal logits), the exact k-th
+// candidate is found by bisection over the tokens themselves.
 //
-// Which thread sums which token depends on the token alone, not on the row's address, so equal
+// Which lane sums which token depends on the token alone, not on the row's address, so equal
 // rows get equal sums and ties between their beams stay ties.
 #include <float.h>
 #include <math.h>
@@ -27,35 +27,35 @@
 namespace tr {
 namespace {
 
-constexpr int kChunkThreads = 256;
-constexpr int kVecs = 8;                 // 16-byte vectors per thread
-constexpr int kMergeThreads = 512;
-constexpr int kMergeCap = 2048;          // candidates the final sort takes
+constexpr int kSumThreads = 256;
+constexpr int kVecs = 8;                 // 16-byte vectors per lane
+constexpr int kPickThreads = 512;
+constexpr int kPickTiles = 1024, kPickGroups = 1023;   // tiles and groups noted for a closer look
+constexpr int kPickCap = 1536;           // candidates the final sort takes
 constexpr int kTokenBits = 24;
 
-template <typename T> struct Vec { static constexpr int N = 16 / sizeof(T); };
-template <typename T> constexpr int chunk_elems() { return kChunkThreads * kVecs * Vec<T>::N; }
+template <typename T> constexpr int tile_elems() { return 32 * kVecs * (16 / (int)sizeof(T)); }
 
-// Order-preserving keys (no NaN reaches them).
+// Order-preserving keys (no NaN reaches them; -0 equals 0).
 __device__ __forceinline__ uint32_t okey(float f) {
-  const uint32_t u = __float_as_uint(f);
+  const uint32_t u = __float_as_uint(f + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ unsigned long long okey(double d) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(d);
+  const unsigned long long u = (unsigned long long)__double_as_longlong(d + 0.0);
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;                      // okey(-inf)
-constexpr unsigned long long kKeyNegInf64 = 0x000FFFFFFFFFFFFFull;
+__device__ __forceinline__ double of_key(unsigned long long k) {
+  return __longlong_as_double((long long)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
+}
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-struct ChunkStat {
-  double sum;      // sum of exp(x - max) over the chunk
+struct __align__(16) TileSum {
   float max;
-  int count;       // candidates listed
-};
-struct Cand {
-  float x;
-  int token;
+  float sum;       // of exponentials, relative to the maximum (see sum_ref)
+  float best;      // the largest logit that may be selected
+  float pad;
 };
 
 struct SelectParams {
@@ -66,9 +66,10 @@ struct SelectParams {
   const uint32_t* allowed;
   int64_t allowed_ld;
   int W, V, k, pad_token;
-  int n_chunk, cap;
-  ChunkStat* stat;     // [rows][n_chunk]
-  Cand* cand;          // [rows][n_chunk][cap]
+  int n_tile;
+  bool aligned;        // every row at a 16-byte aligned address
+  TileSum* sums;       // [rows][n_tile]
+  float* best;         // [rows][n_tile][32]: the groups' largest logits that may be selected
   int32_t *parent, *token;
   float* score;
 };
@@ -78,205 +79,196 @@ __device__ __forceinline__ bool row_offers(const SelectParams& p, int64_t row) {
   return isfinite(c) && !(p.finished && p.finished[row]);
 }
 
-// One 16-byte vector of tokens v .. v + N - 1 of a row, missing tokens as -inf, NaN as -inf.
-template <typename T>
-__device__ __forceinline__ void load_vec(const T* row, int v, int V, float* x) {
-  constexpr int N = Vec<T>::N;
-  T t[N];
-  const T* p = row + v;
-  if (v + N <= V) {
-    const unsigned a = (unsigned)(uintptr_t)row & 15u;   // the same for the whole row
-    if (a == 0) {
-      *reinterpret_cast<uint4*>(t) = __ldcs(reinterpret_cast<const uint4*>(p));
-    } else if ((a & 3) == 0) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) t[i] = p[i];
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = fmaxf(to_f32(t[i]), -INFINITY);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = v + i < V ? fmaxf(to_f32(p[i]), -INFINITY) : -INFINITY;
-  }
+// Sums of exponentials are held as sum_i 2^(x_i log2 e - ref), ref the rounded log2 of the
+// largest term m: subtracting a whole number costs the exponent one rounding of its own size,
+// where a subtraction of m log2 e would shift all terms alike by its rounding and so move one
+// beam's total against another's.  The low part of log2 e is applied to the sum, as 2^(m lo); what
+// is left of it, (x_i - m) lo, is below 2^-22 for every term that counts.  Logits beyond 1e9 in size are
+// further apart than any exponential reaches: there the sum counts the largest logit's copies
+// (infinite ones too).
+constexpr float kHuge = 1e9f;
+constexpr float kL2eHi = 1.4426950408889634f;                 // rounds to 1.44269502...
+constexpr float kL2eLo = (float)(1.4426950408889634 - (double)kL2eHi);
+__device__ __forceinline__ bool huge(float m) { return fabsf(m) > kHuge; }
+__device__ __forceinline__ float sum_ref(float m) { return rintf(m * kL2eHi); }
+// The factor that takes a sum relative to `m` to one relative to `to` (to >= m): a power of two, 0
+// or 1, so exact; terms below 2^-126 of the largest are dropped.
+__device__ __forceinline__ float sum_scale(float m, float to) {
+  if (m == to) return 1.f;
+  if (m == -INFINITY || huge(m) || huge(to)) return 0.f;
+  const float n = sum_ref(m) - sum_ref(to);
+  return n < -126.f ? 0.f : __int_as_float((127 + (int)n) << 23);
+}
+__device__ __forceinline__ double log_sum(float m, double sum) {   // log sum_i exp(x_i)
+  return huge(m) ? (double)m + log(sum) : 0.6931471805599453 * ((double)sum_ref(m) + log2(sum));
 }
 
-// exp(x - m) with -inf - -inf and inf - inf read as 0 (the limit of equal infinite logits).
-__device__ __forceinline__ float exp_diff(float x, float m) { return x == m ? 1.f : __expf(x - m); }
+__device__ __forceinline__ uint64_t pack2f(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split2f(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
+// The registers of a 16-byte vector of logits: four words of two bf16 or of one fp32.  NaN reads
+// as -inf, and so does what lies past the row.
+template <typename T> struct Pack;
+template <> struct Pack<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kNone = 0xFF80FF80u;      // (-inf, -inf)
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {      // elementwise, NaN loses
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ float top(uint32_t w) { return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+  static __device__ __forceinline__ float at(uint32_t w, int e) { return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16); }
+  // of the pair in w: elements whose bit is clear become -inf
+  static __device__ __forceinline__ uint32_t mask(uint32_t w, uint32_t bits) {
+    const uint32_t lo = bits & 1u ? w & 0xFFFFu : 0xFF80u, hi = bits & 2u ? w & 0xFFFF0000u : 0xFF800000u;
+    return lo | hi;
+  }
+};
+template <> struct Pack<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+  static __device__ __forceinline__ float top(uint32_t w) { return __uint_as_float(w); }
+  static __device__ __forceinline__ float at(uint32_t w, int) { return __uint_as_float(w); }
+  static __device__ __forceinline__ uint32_t mask(uint32_t w, uint32_t bits) { return bits & 1u ? w : kNone; }
+};
+
+// A vector that the row ends in, or of a row at an odd address.
 template <typename T>
-__global__ void __launch_bounds__(kChunkThreads) beam_chunk_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int N = Vec<T>::N;
-  const int64_t row = blockIdx.x / p.n_chunk;
-  const int chunk = (int)(blockIdx.x % p.n_chunk);
-  if (!row_offers(p, row)) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const T* lr = static_cast<const T*>(p.logits) + row * p.ld;
-  const int v0 = chunk * chunk_elems<T>() + tid * N;
-  constexpr int kStep = kChunkThreads * N;
-  float x[kVecs][N];
+__device__ __noinline__ uint4 load_partial(const T* p, int n) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) load_vec<T>(lr, v0 + i * kStep, p.V, x[i]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = i < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : Pack<T>::kNone;
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + 2 * i;
+      w[i] = 2 * i < n ? (uint32_t)__ldg(h) : 0xFF80u;
+      w[i] |= 2 * i + 1 < n ? (uint32_t)__ldg(h + 1) << 16 : 0xFF800000u;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Tokens v .. of a row, missing ones as -inf.  kAlign: the row's alignment in bytes, 16, 4 or 2.
+template <typename T, int kAlign>
+__device__ __forceinline__ uint4 load_vec(const T* row, int v, int V) {
+  const T* p = row + v;
+  if (v + Pack<T>::N <= V) {
+    if constexpr (kAlign == 16) {
+      return __ldg(reinterpret_cast<const uint4*>(p));
+    } else if constexpr (kAlign == 4) {
+      const uint32_t* h = reinterpret_cast<const uint32_t*>(p);
+      return make_uint4(__ldg(h), __ldg(h + 1), __ldg(h + 2), __ldg(h + 3));
+    }
+  }
+  if (v < V) return load_partial<T>(p, V - v);
+  return make_uint4(Pack<T>::kNone, Pack<T>::kNone, Pack<T>::kNone, Pack<T>::kNone);
+}
+// The mask bits of tokens v .. (v a multiple of 4 or 8, which divide 32: one word).
+__device__ __forceinline__ uint32_t allowed_bits(const SelectParams& p, int64_t row, int v) {
+  return v < p.V ? __ldg(p.allowed + row * p.allowed_ld + (v >> 5)) >> (v & 31) : 0u;
+}
 
-  // the thread's maximum and sum, then the chunk's
-  float m = -INFINITY;
+template <typename T, int kAlign>
+__global__ void __launch_bounds__(kSumThreads, 4) beam_sum_kernel(const __grid_constant__ SelectParams p) {
+  using P = Pack<T>;
+  constexpr int N = P::N, PER = N / 4;                  // elements per vector, per word
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x & 31, tile = blockIdx.y * (kSumThreads / 32) + (threadIdx.x >> 5);
+  if (tile >= p.n_tile || !row_offers(p, row)) return;
+  const T* lr = static_cast<const T*>(p.logits) + row * p.ld;
+  const int v0 = tile * tile_elems<T>() + lane * N;
+  uint32_t x[kVecs][4];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const uint4 q = load_vec<T, kAlign>(lr, v0 + i * 32 * N, p.V);
+    x[i][0] = q.x; x[i][1] = q.y; x[i][2] = q.z; x[i][3] = q.w;
+  }
+  uint32_t bits[kVecs];
+  if (p.allowed) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) bits[i] = allowed_bits(p, row, v0 + i * 32 * N);
+  }
+  uint32_t top = P::kNone;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-    for (int e = 0; e < N; ++e) m = fmaxf(m, x[i][e]);
+    for (int e = 0; e < 4; ++e) top = P::max(top, x[i][e]);
+  const float m = P::top(top);
   float s = 0.f;
-  if (m > -INFINITY) {
+  const float ref = -sum_ref(m);
+  if (!huge(m)) {
+    const uint64_t ref2 = pack2f(ref, ref), hi2 = pack2f(kL2eHi, kL2eHi);
+    uint64_t sum[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e) s += exp_diff(x[i][e], m);
-  }
-  float gm = m;       // the maximum among the tokens that may be selected
-  if (p.allowed) {
-    const uint32_t* al = p.allowed + row * p.allowed_ld;
-    gm = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int v = v0 + i * kStep;   // a multiple of N, which divides 32: one word
-      const uint32_t bits = v < p.V ? __ldg(al + (v >> 5)) >> (v & 31) : 0u;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        if (!((bits >> e) & 1u)) x[i][e] = -INFINITY;
-        gm = fmaxf(gm, x[i][e]);
+      for (int e = 0; e < 4; e += 2 / PER) {
+        const uint64_t a = PER == 2 ? pack2f(P::at(x[i][e], 0), P::at(x[i][e], 1))
+                                    : pack2f(__uint_as_float(x[i][e]), __uint_as_float(x[i][(e + 1) & 3]));
+        float t0, t1;
+        split2f(fma2(a, hi2, ref2), t0, t1);
+        sum[i & 1] = add2(sum[i & 1], pack2f(ex2(t0), ex2(t1)));
       }
-    }
-  }
-  __shared__ float sm_m[kChunkThreads / 32], sm_hi[kChunkThreads / 32];
-  __shared__ double sm_s[kChunkThreads / 32];
-  __shared__ int sm_count, sm_scan[kChunkThreads / 32];
-  extern __shared__ Cand sm_cand[];                 // [cap]
-  float wm = m, wh = gm;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-    wh = fmaxf(wh, __shfl_xor_sync(0xffffffffu, wh, o));
-  }
-  double ws = m > -INFINITY ? (double)s * (double)exp_diff(m, wm) : 0.0;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-  if (lane == 0) {
-    sm_m[warp] = wm;
-    sm_s[warp] = ws;
-    sm_hi[warp] = wh;
-  }
-  if (tid == 0) sm_count = 0;
-  __syncthreads();
-  float bm = -INFINITY, hi_x = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kChunkThreads / 32; ++w) {
-    bm = fmaxf(bm, sm_m[w]);
-    hi_x = fmaxf(hi_x, sm_hi[w]);
-  }
-  ChunkStat* st = p.stat + row * p.n_chunk + chunk;
-  if (tid == 0) {
-    double tot = 0.0;
-    for (int w = 0; w < kChunkThreads / 32; ++w)
-      if (sm_m[w] > -INFINITY) tot += sm_s[w] * (double)exp_diff(sm_m[w], bm);
-    st->max = bm;
-    st->sum = tot;
-  }
-  // ---- the threshold: the largest found key that at least k thread maxima reach
-  const uint32_t mykey = okey(gm);
-  const int k = p.k;
-  uint32_t lo = kKeyNegInf + 1, hi = okey(hi_x);
-  const int valid = __syncthreads_count(mykey > kKeyNegInf);
-  if (valid >= k) {
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo + 1) / 2;
-      const int c = __syncthreads_count(mykey >= mid);
-      if (c >= k) {
-        lo = mid;
-        if (c <= k + (k >> 3)) break;
-      } else {
-        hi = mid - 1;
-      }
-    }
-  }
-  // ---- list what reaches it
-  Cand* out = p.cand + (row * p.n_chunk + chunk) * (int64_t)p.cap;
-  if (mykey >= lo) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (okey(x[i][e]) >= lo) {
-          const int at = atomicAdd(&sm_count, 1);
-          if (at < p.cap) sm_cand[at] = Cand{x[i][e], v0 + i * kStep + e};
-        }
-  }
-  __syncthreads();
-  int count = sm_count;
-  if (count > p.cap) {
-    // too many: the exact k-th key, everything above it, and its ties in token order
-    uint32_t a = lo, b = okey(hi_x);
-    while (a < b) {
-      const uint32_t mid = a + (b - a + 1) / 2;
-      int c = 0;
+    float t0, t1;
+    split2f(add2(sum[0], sum[1]), t0, t1);
+    s = t0 + t1;
+    if (s != s) {                                       // a NaN logit: leave it out
+      s = 0.f;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-        for (int e = 0; e < N; ++e) c += okey(x[i][e]) >= mid;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0) sm_scan[warp] = c;
-      __syncthreads();
-      int tot = 0;
-      for (int w = 0; w < kChunkThreads / 32; ++w) tot += sm_scan[w];
-      __syncthreads();
-      if (tot >= k) a = mid; else b = mid - 1;
+        for (int e = 0; e < N; ++e) {
+          const float y = P::at(x[i][e / PER], e);
+          if (y == y) s += ex2(fmaf(y, kL2eHi, ref));
+        }
     }
-    if (tid == 0) sm_count = 0;
-    __syncthreads();
+    s *= fmaf(m, kL2eLo * 0.693147f, 1.f);
+  } else if (m > -INFINITY) {                           // (of all -inf the sum is unused)
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (okey(x[i][e]) > a) sm_cand[atomicAdd(&sm_count, 1)] = Cand{x[i][e], v0 + i * kStep + e};   // fewer than k
-    __syncthreads();
-    int have = sm_count;
-    for (int i = 0; i < kVecs && have < k; ++i) {      // `have` is the same in every thread
-      int mine = 0;
-#pragma unroll
-      for (int q = 0; q < kVecs; ++q)
-        if (q == i)
-#pragma unroll
-          for (int e = 0; e < N; ++e) mine += okey(x[q][e]) == a;
-      int incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) sm_scan[warp] = incl;
-      __syncthreads();
-      int at = have + incl - mine, tot = 0;
-      for (int w = 0; w < kChunkThreads / 32; ++w) {
-        if (w < warp) at += sm_scan[w];
-        tot += sm_scan[w];
-      }
-#pragma unroll
-      for (int q = 0; q < kVecs; ++q)
-        if (q == i)
-#pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (okey(x[q][e]) == a) {
-              if (at < k) sm_cand[at] = Cand{x[q][e], v0 + i * kStep + e};
-              ++at;
-            }
-      have += tot;
-      __syncthreads();
-    }
-    count = min(have, k);
+      for (int e = 0; e < N; ++e) s += P::at(x[i][e / PER], e) == m ? 1.f : 0.f;
   }
-  for (int i = tid; i < count; i += kChunkThreads) out[i] = sm_cand[i];
-  if (tid == 0) st->count = count;
+  if (p.allowed) {
+    top = P::kNone;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = P::max(top, P::mask(x[i][e], bits[i] >> (e * PER)));
+  }
+  const float wm = of_key(__reduce_max_sync(0xffffffffu, okey(m)));
+  float ws = s * sum_scale(m, wm);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+  const int64_t at = row * p.n_tile + tile;
+  const float gm = P::top(top);
+  const float wg = p.allowed ? of_key(__reduce_max_sync(0xffffffffu, okey(gm))) : wm;
+  p.best[at * 32 + lane] = gm;
+  if (lane == 0) *reinterpret_cast<float4*>(p.sums + at) = make_float4(wm, ws, wg, 0.f);
 }
 
 // A candidate's place: total first, then lower beam, higher logit, lower token.
@@ -291,90 +283,293 @@ __device__ __forceinline__ unsigned long long tie_of(int beam, float x, int toke
          (unsigned long long)((1 << kTokenBits) - 1 - token);
 }
 
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ float s_max[TR_MAX_BEAMS];
-  __shared__ double s_logsum[TR_MAX_BEAMS];
-  __shared__ int s_kind[TR_MAX_BEAMS];            // 0 dead, 1 offers tokens, 2 finished
-  __shared__ unsigned long long s_hi;
-  __shared__ int s_count;
-  extern __shared__ Rank s_rank[];                // [kMergeCap]
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// One warp, n keys per lane: a key, at least `floor`, that at least `want` of them reach (that many
+// are known to reach `floor`), and not many more than that.  A step tries three keys, whose counts (at
+// most 512 each) share one reduction.
+template <int n, typename F>
+__device__ __forceinline__ uint32_t bisect(F load, int want, uint32_t floor) {
+  uint32_t key[n], a = ~0u, b = 0;
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    key[i] = load(i);
+    a = min(a, max(key[i], floor));
+    b = max(b, key[i]);
+  }
+  a = __reduce_min_sync(0xffffffffu, a);
+  b = max(a, __reduce_max_sync(0xffffffffu, b));
+  while (a < b) {
+    const uint32_t q = (b - a + 3) / 4, m1 = min(a + q, b), m2 = min(m1 + q, b), m3 = min(m2 + q, b);
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) c += (key[i] >= m1 ? 1u : 0u) + (key[i] >= m2 ? 1u << 10 : 0u) + (key[i] >= m3 ? 1u << 20 : 0u);
+    c = __reduce_add_sync(0xffffffffu, c);
+    const int c1 = c & 1023, c2 = c >> 10 & 1023, c3 = c >> 20;
+    int got = 0;
+    if (c3 >= want) {
+      a = m3;
+      got = c3;
+    } else if (c2 >= want) {
+      a = m2;
+      b = m3 - 1;
+      got = c2;
+    } else if (c1 >= want) {
+      a = m1;
+      b = m2 - 1;
+      got = c1;
+    } else {
+      b = m1 - 1;
+    }
+    if (got && got <= want + (want >> 3) + 8) break;
+  }
+  return a;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ SelectParams p) {
+  using P = Pack<T>;
+  constexpr int N = P::N, kWarps = kPickThreads / 32;
+  __shared__ float s_max[TR_MAX_BEAMS], s_off[TR_MAX_BEAMS];
+  __shared__ double s_lse[TR_MAX_BEAMS], s_cum[TR_MAX_BEAMS];
+  __shared__ uint8_t s_kind[TR_MAX_BEAMS];        // 0 dead, 1 offers tokens, 2 finished
+  __shared__ uint32_t s_key[kPickCap], s_best[kPickThreads], s_cut;
+  __shared__ __align__(16) uint32_t s_sel_key[kPickCap];
+  __shared__ float s_up[kPickGroups];
+  __shared__ int s_count, s_tiles, s_groups, s_tile[kPickTiles], s_group[kPickGroups];
+  extern __shared__ Rank s_rank[];                // [kPickCap]
+  int* s_sel = reinterpret_cast<int*>(s_rank + kPickCap);
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.k;
   const int64_t row0 = (int64_t)r * p.W;
-  for (int b = tid; b < p.W; b += kMergeThreads) {
-    const int64_t row = row0 + b;
-    int kind = 0;
+  const TileSum* sums = p.sums + row0 * p.n_tile;
+  // ---- a warp per beam: the row's maximum and sum, then a thread per beam: its log-sum-exp
+  for (int b = warp; b < p.W; b += kWarps) {
+    const float cum = p.cum[row0 + b];
+    int kind = isfinite(cum) ? p.finished && p.finished[row0 + b] ? 2 : 1 : 0;
     float M = -INFINITY;
     double S = 0.0;
-    if (isfinite(p.cum[row])) {
-      if (p.finished && p.finished[row]) {
-        kind = 2;
-      } else {
-        const ChunkStat* st = p.stat + row * p.n_chunk;
-        for (int c = 0; c < p.n_chunk; ++c) M = fmaxf(M, st[c].max);
-        for (int c = 0; c < p.n_chunk; ++c)
-          if (st[c].max > -INFINITY) S += st[c].sum * (st[c].max == M ? 1.0 : exp((double)st[c].max - (double)M));
-        kind = M > -INFINITY ? 1 : 0;
+    if (kind == 1) {
+      constexpr int kHeld = 4;                          // tiles per lane held between the two steps
+      float4 y[kHeld];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        y[i] = lane + 32 * i < p.n_tile ? __ldg(reinterpret_cast<const float4*>(sums + b * p.n_tile + lane + 32 * i))
+                                        : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) M = fmaxf(M, y[i].x);
+      for (int c = lane + 32 * kHeld; c < p.n_tile; c += 32) M = fmaxf(M, __ldg(&sums[b * p.n_tile + c].max));
+      M = of_key(__reduce_max_sync(0xffffffffu, okey(M)));
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) S += (double)(y[i].y * sum_scale(y[i].x, M));
+      for (int c = lane + 32 * kHeld; c < p.n_tile; c += 32) {
+        const float4 z = __ldg(reinterpret_cast<const float4*>(sums + b * p.n_tile + c));
+        S += (double)(z.y * sum_scale(z.x, M));
       }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+      if (M == -INFINITY) kind = 0;
     }
-    s_kind[b] = kind;
-    s_max[b] = M;
-    s_logsum[b] = kind == 1 ? log(S) : 0.0;
+    if (lane == 0) {
+      s_kind[b] = (uint8_t)kind;
+      s_max[b] = M;
+      s_cum[b] = (double)cum;
+      s_lse[b] = S;
+    }
   }
-  if (tid == 0) {
-    s_hi = 0;
-    s_count = 0;
+  if (tid == 0) s_count = s_tiles = s_groups = 0;
+  __syncthreads();
+  if (tid < p.W) {
+    const float M = s_max[tid];
+    const double lse = s_kind[tid] != 1 ? 0.0 : huge(M) ? log(s_lse[tid]) : log_sum(M, s_lse[tid]);
+    s_lse[tid] = lse;
+    s_off[tid] = (float)(s_cum[tid] - (s_kind[tid] != 1 || huge(M) ? lse : lse - (double)M));
   }
   __syncthreads();
-  const int n_list = p.W * p.n_chunk;
-  constexpr int kWarps = kMergeThreads / 32;
-  // f(rank) for every candidate of this thread
-  auto each = [&](auto f) {
-    for (int l = warp; l < n_list; l += kWarps) {
-      const int b = l / p.n_chunk;
-      const int64_t row = row0 + b;
-      if (s_kind[b] == 1) {
-        const int cnt = p.stat[row0 * p.n_chunk + l].count;
-        const Cand* c = p.cand + (row0 * p.n_chunk + l) * (int64_t)p.cap;
-        const double cum = p.cum[row], ls = s_logsum[b];
-        const float M = s_max[b];
-        for (int i = lane; i < cnt; i += 32) {
-          const Cand q = c[i];
-          const double d = q.x == M ? 0.0 : (double)q.x - (double)M;
-          if (d > -INFINITY) f(Rank{okey(cum + (d - ls)), tie_of(b, q.x, q.token)});
+  // ---- totals.  Exactly, as a 64-bit key (0: not a candidate):
+  auto key_of = [&](int b, float x) -> unsigned long long {
+    const float M = s_max[b];
+    const double d = huge(M) ? (x == M ? 0.0 : (double)x - (double)M) : (double)x;
+    const double t = s_cum[b] + (d - s_lse[b]);
+    return t > -INFINITY ? okey(t) : 0ull;
+  };
+  // In fp32, t, off by at most e: a difference and a sum of two terms, each of which was rounded
+  // once, so 2^-22 of their sizes covers them.
+  struct Near { float t, e; };
+  auto near_of = [&](int b, float x) -> Near {
+    const float M = s_max[b], off = s_off[b], d = x == M ? 0.f : x - M;
+    return Near{d + off, 0x1p-22f * (fabsf(d) + fabsf(off))};
+  };
+  const int per_row = p.n_tile * 32, n_tile = p.W * p.n_tile, n_group = p.W * per_row;
+  const float* best = p.best + row0 * per_row;
+  // f(beam, tile of the row, t, e) for this thread's tiles; a finished beam counts as its first
+  auto each_tile = [&](auto f) {
+#pragma unroll 2
+    for (int j = tid; j < n_tile; j += kPickThreads) {
+      const int b = j / p.n_tile, kind = s_kind[b];
+      if (kind == 1) {
+        const float x = __ldg(&sums[j].best);
+        if (x > -INFINITY) {
+          const Near y = near_of(b, x);
+          f(b, j - b * p.n_tile, y.t, y.e);
         }
-      } else if (s_kind[b] == 2 && l % p.n_chunk == 0 && lane == 0) {
-        f(Rank{okey((double)p.cum[row]), tie_of(b, 0.f, p.pad_token)});
+      } else if (kind == 2 && j % p.n_tile == 0) {
+        f(b, 0, s_off[b], 0.f);
       }
     }
   };
-  unsigned long long mine = 0;
-  each([&](const Rank& q) {
-    if (q.key > mine) mine = q.key;
-  });
-  if (mine) atomicMax(&s_hi, mine);
-  const int k = p.k;
-  const int valid = __syncthreads_count(mine != 0);
-  unsigned long long lo = kKeyNegInf64 + 1, hi = s_hi;
-  if (valid >= k)
-    while (lo < hi) {
-      const unsigned long long mid = lo + (hi - lo + 1) / 2;
-      const int c = __syncthreads_count(mine >= mid);
-      if (c >= k) {
-        lo = mid;
-        if (c <= k + (k >> 3)) break;
-      } else {
-        hi = mid - 1;
+  // f(beam, group of the row, t, e) for this thread's groups, four neighbours at a time
+  auto each_group = [&](auto f) {
+    for (int j = tid * 4; j < n_group; j += kPickThreads * 4) {
+      const int b = j / per_row, kind = s_kind[b];
+      if (kind == 1) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(best + j));
+        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (y[e] > -INFINITY) {
+            const Near u = near_of(b, y[e]);
+            f(b, j - b * per_row + e, u.t, u.e);
+          }
+      } else if (kind == 2 && j % per_row == 0) {
+        f(b, 0, s_off[b], 0.f);
       }
     }
-  each([&](const Rank& q) {
-    if (q.key >= lo) {
-      const int at = atomicAdd(&s_count, 1);
-      if (at < kMergeCap) s_rank[at] = q;
+  };
+  // A bound that at least k totals reach, from the threads' best (lower ends of) totals; false when
+  // fewer than k threads have one.
+  uint32_t lo = kKeyNegInf + 1;
+  float upper;
+  auto bound_of = [&](auto&& each) {
+    float mine = -INFINITY;
+    upper = -INFINITY;
+    each([&](int, int, float t, float e) {
+      mine = fmaxf(mine, t - e);
+      upper = fmaxf(upper, t + e);
+    });
+    s_key[tid] = okey(mine);
+    if (__syncthreads_count(mine > -INFINITY) < k) return false;
+    if (warp == 0) {
+      const uint32_t cut = bisect<kPickThreads / 32>([&](int i) { return s_key[i * 32 + lane]; }, k, lo);
+      if (lane == 0) s_cut = cut;
     }
+    __syncthreads();
+    lo = s_cut;
+    return true;
+  };
+  float bound = of_key(lo);
+  // ---- the groups that may hold a token that reaches it, by way of the tiles
+  auto note = [&](int b, int i, float t, float e) {
+    if (t + e >= bound) {
+      const int at = atomicAdd(&s_groups, 1);
+      if (at < kPickGroups) {
+        s_group[at] = b << 19 | i;
+        s_key[at] = okey(t - e);
+        s_up[at] = t + e;
+      }
+    }
+  };
+  bool by_tile = bound_of(each_tile);
+  if (by_tile) {
+    bound = of_key(lo);
+    if (upper >= bound)
+      each_tile([&](int b, int i, float t, float e) {
+        if (t + e >= bound) {
+          const int at = atomicAdd(&s_tiles, 1);
+          if (at < kPickTiles) s_tile[at] = b << 14 | i;
+        }
+      });
+    __syncthreads();
+    by_tile = s_tiles <= kPickTiles;
+  }
+  if (by_tile) {
+    constexpr int kAhead = 4;
+    for (int i0 = warp; i0 < s_tiles; i0 += kWarps * kAhead) {
+      float x[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int i = i0 + q * kWarps, w = i < s_tiles ? s_tile[i] : 0, b = w >> 14;
+        x[q] = i < s_tiles && s_kind[b] == 1 ? __ldg(best + b * per_row + (w & 16383) * 32 + lane) : -INFINITY;
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int i = i0 + q * kWarps;
+        if (i >= s_tiles) break;
+        const int w = s_tile[i], b = w >> 14;
+        if (s_kind[b] == 2) {
+          if (lane == 0) note(b, 0, s_off[b], 0.f);
+        } else if (x[q] > -INFINITY) {
+          const Near y = near_of(b, x[q]);
+          note(b, (w & 16383) * 32 + lane, y.t, y.e);
+        }
+      }
+    }
+  } else {
+    each_group(note);
+  }
+  __syncthreads();
+  if (s_groups > kPickGroups) {
+    // too many to note: a bound from the groups themselves, and once more
+    bound_of(each_group);
+    bound = of_key(lo);
+    if (tid == 0) s_groups = 0;
+    __syncthreads();
+    each_group(note);
+    __syncthreads();
+  }
+  const bool noted = s_groups <= kPickGroups;
+  if (noted && s_groups > k + (k >> 2) + 16) {
+    // the k-th best of the noted groups is a better bound
+    const int n = s_groups;
+    for (int i = n + tid; i < kPickGroups + 1; i += kPickThreads) s_key[i] = 0u;
+    __syncthreads();
+    if (warp == 0) {
+      const uint32_t cut = bisect<(kPickGroups + 1) / 32>([&](int i) { return s_key[i * 32 + lane]; }, k, lo);
+      if (lane == 0) s_cut = cut;
+    }
+    __syncthreads();
+    lo = s_cut;
+    bound = of_key(lo);
+  }
+  const int n_scan = (noted ? s_groups : n_group) * kVecs;
+  // f(rank) for every token of those groups that may reach the bound: a vector at a time
+  auto each = [&](auto f) {
+    for (int j = tid; j < n_scan; j += kPickThreads) {
+      int b, i;
+      if (noted) {
+        if (s_up[j / kVecs] < bound) continue;
+        b = s_group[j / kVecs] >> 19;
+        i = s_group[j / kVecs] & ((1 << 19) - 1);
+      } else {
+        b = j / kVecs / per_row;
+        i = j / kVecs % per_row;
+      }
+      const int kind = s_kind[b];
+      if (kind == 2 && i == 0 && j % kVecs == 0) f(Rank{okey(s_cum[b]), tie_of(b, 0.f, p.pad_token)});
+      if (kind != 1) continue;
+      const int v = (i / 32) * tile_elems<T>() + (j % kVecs) * 32 * N + (i % 32) * N;
+      if (v >= p.V) continue;
+      const T* lr = static_cast<const T*>(p.logits) + (row0 + b) * p.ld;
+      const uint4 q = p.aligned ? load_vec<T, 16>(lr, v, p.V) : load_partial<T>(lr + v, p.V - v);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const uint32_t bits = p.allowed ? allowed_bits(p, row0 + b, v) : ~0u;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float x = P::at(w[e / (N / 4)], e);
+        if (x > -INFINITY && (bits >> e & 1u)) {
+          const Near y = near_of(b, x);
+          if (y.t + y.e >= bound) {
+            const unsigned long long key = key_of(b, x);
+            if (key) f(Rank{key, tie_of(b, x, v + e)});
+          }
+        }
+      }
+    }
+  };
+  each([&](const Rank& q) {
+    const int at = atomicAdd(&s_count, 1);
+    if (at < kPickCap) s_rank[at] = q;
   });
   __syncthreads();
   int count = s_count;
-  if (count > kMergeCap) {
+  if (count > kPickCap) {
     // too many: the exact k-th candidate, by its total and then by its tie
     auto count_if = [&](auto pred) {
       int c = 0;
@@ -387,9 +582,9 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
       __syncthreads();
       return s_count;
     };
-    unsigned long long a = lo, b = s_hi;
+    unsigned long long a = 1, b = ~0ull;
     while (a < b) {
-      const unsigned long long mid = a + (b - a + 1) / 2;
+      const unsigned long long mid = a + (b - a) / 2 + 1;
       if (count_if([&](const Rank& q) { return q.key >= mid; }) >= k) a = mid; else b = mid - 1;
     }
     unsigned long long ta = 0, tb = ~0ull;
@@ -406,37 +601,59 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     __syncthreads();
     count = s_count;
   }
-  int n = 1;
-  while (n < count) n <<= 1;
-  for (int i = count + tid; i < n; i += kMergeThreads) s_rank[i] = Rank{0ull, 0ull};
-  __syncthreads();
-  for (int size = 2; size <= n; size <<= 1)
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      for (int i = tid; i < n; i += kMergeThreads) {
-        const int j = i ^ stride;
-        if (j > i) {
-          const Rank a = s_rank[i], b = s_rank[j];
-          if ((i & size) == 0 ? before(b, a) : before(a, b)) {
-            s_rank[i] = b;
-            s_rank[j] = a;
-          }
-        }
+  // the totals rounded to fp32 order the candidates but for ties; those that may be among the k best
+  uint32_t cut = 0u, mykey = 0u;
+  for (int i = tid; i < count; i += kPickThreads) mykey = max(mykey, s_key[i] = okey((float)of_key(s_rank[i].key)));
+  if (tid == 0) s_groups = 0;
+  if (count > 2 * k + 32) {
+    s_best[tid] = mykey;
+    if (__syncthreads_count(mykey > 0u) >= k) {
+      if (warp == 0) {
+        const uint32_t c = bisect<kPickThreads / 32>([&](int i) { return s_best[i * 32 + lane]; }, k, 1u);
+        if (lane == 0) s_cut = c;
       }
       __syncthreads();
+      cut = s_cut;
     }
-  for (int j = tid; j < k; j += kMergeThreads) {
-    int par = -1, tok = -1;
-    float sc = -INFINITY;
-    if (j < count) {
-      const Rank q = s_rank[j];
-      par = 255 - (int)(q.tie >> 56);
-      tok = (1 << kTokenBits) - 1 - (int)(q.tie & ((1u << kTokenBits) - 1));
-      const unsigned long long u = q.key;
-      sc = (float)__longlong_as_double((long long)((u >> 63) ? (u & 0x7FFFFFFFFFFFFFFFull) : ~u));
+  }
+  __syncthreads();
+  for (int i = tid; i < count; i += kPickThreads)
+    if (s_key[i] >= cut) {
+      const int at = atomicAdd(&s_groups, 1);
+      s_sel[at] = i;
+      s_sel_key[at] = s_key[i];
     }
-    p.parent[(int64_t)r * k + j] = par;
-    p.token[(int64_t)r * k + j] = tok;
-    p.score[(int64_t)r * k + j] = sc;
+  __syncthreads();
+  const int n_sel = s_groups;
+  if (tid < (-n_sel & 3)) s_sel_key[n_sel + tid] = 0u;
+  __syncthreads();
+  auto put = [&](int j, const Rank& q) {
+    const int64_t at = (int64_t)r * k + j;
+    p.parent[at] = 255 - (int)(q.tie >> 56);
+    p.token[at] = (1 << kTokenBits) - 1 - (int)(q.tie & ((1u << kTokenBits) - 1));
+    p.score[at] = (float)of_key(q.key);
+  };
+  // each of them counts those before it
+  const uint4* key4 = reinterpret_cast<const uint4*>(s_sel_key);
+  for (int i = tid; i < n_sel; i += kPickThreads) {
+    const uint32_t key = s_sel_key[i];
+    int at = 0, same = 0;
+#pragma unroll 4
+    for (int j = 0; j < (n_sel + 3) / 4; ++j) {
+      const uint4 o = key4[j];
+      at += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+      same += (o.x == key) + (o.y == key) + (o.z == key) + (o.w == key);
+    }
+    if (at >= k) continue;
+    const Rank q = s_rank[s_sel[i]];
+    if (same > 1)
+      for (int j = 0; j < n_sel; ++j) at += s_sel_key[j] == key && before(s_rank[s_sel[j]], q);
+    if (at < k) put(at, q);
+  }
+  for (int j = count + tid; j < k; j += kPickThreads) {
+    const int64_t at = (int64_t)r * k + j;
+    p.parent[at] = p.token[at] = -1;
+    p.score[at] = -INFINITY;
   }
 }
 
@@ -542,17 +759,34 @@ bool overlap(const Rows& a, const Rows& b) {
 }
 
 struct SelectPlan {
-  int n_chunk, cap;
-  size_t stat_bytes, total;
+  int n_tile;
+  size_t sum_bytes, total;
 };
-SelectPlan plan_select(int64_t rows, int V, int k, bool f32) {
+SelectPlan plan_select(int64_t rows, int V, bool f32) {
   SelectPlan s;
-  const int elems = f32 ? chunk_elems<float>() : chunk_elems<__nv_bfloat16>();
-  s.n_chunk = (V + elems - 1) / elems;
-  s.cap = std::min(std::max(256, 4 * k), elems);
-  s.stat_bytes = ((size_t)rows * s.n_chunk * sizeof(ChunkStat) + 255) / 256 * 256;
-  s.total = s.stat_bytes + (size_t)rows * s.n_chunk * s.cap * sizeof(Cand);
+  const int elems = f32 ? tile_elems<float>() : tile_elems<__nv_bfloat16>();
+  s.n_tile = (V + elems - 1) / elems;
+  s.sum_bytes = ((size_t)rows * s.n_tile * sizeof(TileSum) + 255) / 256 * 256;
+  s.total = s.sum_bytes + (size_t)rows * s.n_tile * 32 * sizeof(float);
   return s;
+}
+
+template <typename T>
+tr_status launch_select(const SelectParams& p, int R, uintptr_t align, cudaStream_t st) {
+  const dim3 grid((unsigned)(R * p.W), (unsigned)((p.n_tile + kSumThreads / 32 - 1) / (kSumThreads / 32)));
+  // rows at 16-byte aligned addresses are read 16 bytes at a time
+  if (align % 16 == 0)
+    beam_sum_kernel<T, 16><<<grid, kSumThreads, 0, st>>>(p);
+  else if (sizeof(T) == 4 || align % 4 == 0)
+    beam_sum_kernel<T, 4><<<grid, kSumThreads, 0, st>>>(p);
+  else
+    beam_sum_kernel<T, 2><<<grid, kSumThreads, 0, st>>>(p);
+  TR_LAUNCH_CHECK("beam_sum_kernel");
+  constexpr int kPickBytes = kPickCap * (sizeof(Rank) + sizeof(int));
+  TR_TRY(ensure_smem_attr((const void*)beam_pick_kernel<T>, kPickBytes));
+  beam_pick_kernel<T><<<R, kPickThreads, kPickBytes, st>>>(p);
+  TR_LAUNCH_CHECK("beam_pick_kernel");
+  return TR_OK;
 }
 
 tr_status check_select(int R, int W, int V, int k) {
@@ -571,7 +805,7 @@ using namespace tr;
 extern "C" size_t tr_beam_select_workspace(int R, int W, int V, int k) {
   if (check_select(R, W, V, k) != TR_OK) return SIZE_MAX;
   const int64_t rows = (int64_t)R * W;
-  return std::max(plan_select(rows, V, k, true).total, plan_select(rows, V, k, false).total);
+  return std::max(plan_select(rows, V, true).total, plan_select(rows, V, false).total);
 }
 
 extern "C" tr_status tr_beam_select(const void* logits, tr_dtype logits_dtype, int64_t ld, const float* cum,
@@ -591,10 +825,9 @@ extern "C" tr_status tr_beam_select(const void* logits, tr_dtype logits_dtype, i
       (uintptr_t)token % 4 || (uintptr_t)score % 4)
     return fail(TR_ERR_INVALID_ARG, "a pointer is not aligned to its type");
   const int64_t rows = (int64_t)R * W;
-  const SelectPlan sp = plan_select(rows, V, k, logits_dtype == TR_F32);
+  const SelectPlan sp = plan_select(rows, V, logits_dtype == TR_F32);
   if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < sp.total)
     return fail(TR_ERR_INVALID_ARG, "workspace: need %zu bytes, 16-byte aligned", sp.total);
-  if (rows * sp.n_chunk > INT32_MAX) return fail(TR_ERR_UNSUPPORTED, "R*W*V is too large for one call");
   const cudaStream_t st = (cudaStream_t)stream;
   SelectParams p{};
   p.logits = logits;
@@ -607,23 +840,15 @@ extern "C" tr_status tr_beam_select(const void* logits, tr_dtype logits_dtype, i
   p.V = V;
   p.k = k;
   p.pad_token = pad_token;
-  p.n_chunk = sp.n_chunk;
-  p.cap = sp.cap;
-  p.stat = static_cast<ChunkStat*>(workspace);
-  p.cand = reinterpret_cast<Cand*>(static_cast<uint8_t*>(workspace) + sp.stat_bytes);
+  p.n_tile = sp.n_tile;
+  p.sums = static_cast<TileSum*>(workspace);
+  p.best = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.sum_bytes);
   p.parent = parent;
   p.token = token;
   p.score = score;
-  const unsigned grid = (unsigned)(rows * sp.n_chunk);
-  const size_t smem = (size_t)sp.cap * sizeof(Cand);
-  if (logits_dtype == TR_F32)
-    beam_chunk_kernel<float><<<grid, kChunkThreads, smem, st>>>(p);
-  else
-    beam_chunk_kernel<__nv_bfloat16><<<grid, kChunkThreads, smem, st>>>(p);
-  TR_LAUNCH_CHECK("beam_chunk_kernel");
-  beam_merge_kernel<<<R, kMergeThreads, kMergeCap * sizeof(Rank), st>>>(p);
-  TR_LAUNCH_CHECK("beam_merge_kernel");
-  return TR_OK;
+  const uintptr_t align = (uintptr_t)logits | (uintptr_t)(rows > 1 ? ld * esize : 0);
+  p.aligned = align % 16 == 0;
+  return logits_dtype == TR_F32 ? launch_select<float>(p, R, align, st) : launch_select<__nv_bfloat16>(p, R, align, st);
 }
 
 extern "C" tr_status tr_beam_reorder(const tr_beam_state* states, int n_states, const int32_t* parent, int R, int W_in,
