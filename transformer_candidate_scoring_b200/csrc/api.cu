@@ -125,6 +125,20 @@ tr_status stream_counters(cudaStream_t st, int** out) {
   return TR_OK;
 }
 
+tr_status sm_count(int* out) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  TR_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(TR_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    TR_CUDA_TRY(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return TR_OK;
+}
+
 tr_status ensure_smem_attr(const void* kernel, int bytes) {
   int dev = 0;
   TR_CUDA_TRY(cudaGetDevice(&dev));

@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.k;
   const int64_t row0 = (int64_t)r * p.W;
   const TileSum* sums = p.sums + row0 * p.n_tile;
+  cudaGridDependencySynchronize();
   // ---- a warp per beam: the row's maximum and sum, then a thread per beam: its log-sum-exp
   for (int b = warp; b < p.W; b += kWarps) {
     const float cum = p.cum[row0 + b];
@@ -351,16 +352,16 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       float4 y[kHeld];
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
-        y[i] = lane + 32 * i < p.n_tile ? __ldg(reinterpret_cast<const float4*>(sums + b * p.n_tile + lane + 32 * i))
+        y[i] = lane + 32 * i < p.n_tile ? __ldcg(reinterpret_cast<const float4*>(sums + b * p.n_tile + lane + 32 * i))
                                         : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) M = fmaxf(M, y[i].x);
-      for (int c = lane + 32 * kHeld; c < p.n_tile; c += 32) M = fmaxf(M, __ldg(&sums[b * p.n_tile + c].max));
+      for (int c = lane + 32 * kHeld; c < p.n_tile; c += 32) M = fmaxf(M, __ldcg(&sums[b * p.n_tile + c].max));
       M = of_key(__reduce_max_sync(0xffffffffu, okey(M)));
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) S += (double)(y[i].y * sum_scale(y[i].x, M));
       for (int c = lane + 32 * kHeld; c < p.n_tile; c += 32) {
-        const float4 z = __ldg(reinterpret_cast<const float4*>(sums + b * p.n_tile + c));
+        const float4 z = __ldcg(reinterpret_cast<const float4*>(sums + b * p.n_tile + c));
         S += (double)(z.y * sum_scale(z.x, M));
       }
 #pragma unroll
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     for (int j = tid; j < n_tile; j += kPickThreads) {
       const int b = j / p.n_tile, kind = s_kind[b];
       if (kind == 1) {
-        const float x = __ldg(&sums[j].best);
+        const float x = __ldcg(&sums[j].best);
         if (x > -INFINITY) {
           const Near y = near_of(b, x);
           f(b, j - b * p.n_tile, y.t, y.e);
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     for (int j = tid * 4; j < n_group; j += kPickThreads * 4) {
       const int b = j / per_row, kind = s_kind[b];
       if (kind == 1) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(best + j));
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(best + j));
         const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int i = i0 + q * kWarps, w = i < s_tiles ? s_tile[i] : 0, b = w >> 14;
-        x[q] = i < s_tiles && s_kind[b] == 1 ? __ldg(best + b * per_row + (w & 16383) * 32 + lane) : -INFINITY;
+        x[q] = i < s_tiles && s_kind[b] == 1 ? __ldcg(best + b * per_row + (w & 16383) * 32 + lane) : -INFINITY;
       }
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
@@ -784,9 +785,7 @@ tr_status launch_select(const SelectParams& p, int R, uintptr_t align, cudaStrea
   TR_LAUNCH_CHECK("beam_sum_kernel");
   constexpr int kPickBytes = kPickCap * (sizeof(Rank) + sizeof(int));
   TR_TRY(ensure_smem_attr((const void*)beam_pick_kernel<T>, kPickBytes));
-  beam_pick_kernel<T><<<R, kPickThreads, kPickBytes, st>>>(p);
-  TR_LAUNCH_CHECK("beam_pick_kernel");
-  return TR_OK;
+  return launch_dependent(beam_pick_kernel<T>, (unsigned)R, kPickThreads, kPickBytes, st, "beam_pick_kernel", p);
 }
 
 tr_status check_select(int R, int W, int V, int k) {

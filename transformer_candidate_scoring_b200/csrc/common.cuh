@@ -58,6 +58,30 @@ tr_status stream_counters(cudaStream_t st, int** out);
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (device, kernel), under a lock.
 tr_status ensure_smem_attr(const void* kernel, int bytes);
 
+// SMs of the current device.
+tr_status sm_count(int* out);
+
+// Launches a kernel that may start before the one launched last on the stream has ended: it calls
+// cudaGridDependencySynchronize() before it touches anything that kernel writes.
+template <typename... Params, typename... Args>
+tr_status launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                           const char* what, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  count_launch();
+  if (e != cudaSuccess) return fail(TR_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));
+  return TR_OK;
+}
+
 // ---------------------------------------------------------------- numeric helpers
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

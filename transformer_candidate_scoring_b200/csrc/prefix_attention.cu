@@ -26,21 +26,9 @@ __device__ __forceinline__ int request_of(const AttnParams& p, int64_t s) {
   return lo;
 }
 
-// Suffix keys that query token t of sequence s sees; a length outside the buffer is clamped.
-__device__ __forceinline__ int visible_suffix(const AttnParams& p, int64_t s, int t) {
-  if (p.d.suffix_cap == 0) return 0;
-  int len = p.suffix_len[s];
-  if (len < 0 || len > p.d.suffix_cap) {
-    if ((threadIdx.x & 31) == 0) atomicOr(p.status, STATUS_KEY_RANGE);
-    len = min(max(len, 0), p.d.suffix_cap);
-  }
-  return p.d.causal ? max(0, len - (p.d.L_t - 1 - t)) : len;
-}
-
 // One warp per (s, t, head): 32 keys at a time, each lane one key's product with the query, then
-// each lane some of the output columns.  With kPartial the prefix part of the row has been
-// computed (launch_prefix_tc): its partial results are merged instead of the prefix being read.
-template <typename T, bool kPartial>
+// each lane some of the output columns.
+template <typename T>
 __global__ void __launch_bounds__(kRowWarps * 32) attn_row_kernel(const __grid_constant__ AttnParams p) {
   __shared__ float sq[kRowWarps][kMaxDHead];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -96,20 +84,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_row_kernel(const __grid_c
     }
   };
   const RequestPlan& rq = p.req[r];
-  if constexpr (kPartial) {
-    const int64_t rows = request_rows(p, r);
-    for (int i = 0; i < rq.n_split; ++i) {
-      const int64_t at = rq.part + i * rows + (row - (int64_t)rq.s0 * p.d.L_t * H);
-      const float z = p.part_lse[at];
-      if (z == -INFINITY) continue;
-      const float nm = fmaxf(m, z), f = exp2f(m - nm), w = exp2f(z - nm);
-      l = l * f + w;
-      m = nm;
-#pragma unroll
-      for (int e = 0; e < kMaxDHead / 32; ++e)
-        if (lane + 32 * e < D) o[e] = o[e] * f + w * p.part_o[at * D + lane + 32 * e];
-    }
-  } else {
+  {
     const int64_t po = rq.p0 * p.d.prefix_token + hk * p.d.prefix_head;
     keys(static_cast<const T*>(p.k_prefix) + po, static_cast<const T*>(p.v_prefix) + po, p.d.prefix_token, rq.p1 - rq.p0);
   }
@@ -122,6 +97,374 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_row_kernel(const __grid_c
   for (int i = 0; i < kMaxDHead / 32; ++i)
     if (lane + 32 * i < D) out[lane + 32 * i] = from_f32<T>(o[i] * inv);
   if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+}
+
+// The suffix part of every row, and the merge with the prefix part's partial results.  A team of
+// kLanes lanes holds a row, eight of its columns per lane; `parts` teams share a row's suffix
+// keys and partial results where rows are few (their results meet in shared memory).  What it
+// must read -- each sequence's own keys and values, the partial results -- bounds it: four keys
+// are in flight per lane, and the suffix part does not wait for the prefix kernel.
+constexpr int kFinishThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* x) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// A softmax row in progress: 2^(a - m) summed, and the values so weighted.
+struct Running {
+  float m = -INFINITY, l = 0.f, o[8] = {};
+  __device__ __forceinline__ void rescale(float nm, float* base) {       // *base: what numerators are relative to
+    *base = nm == -INFINITY ? 0.f : nm;                                  // keys of -inf weigh nothing, NaN stays NaN
+    const float f = exp2f(m - *base);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f;
+    m = nm;
+  }
+  __device__ __forceinline__ float lse() const { return l == 0.f ? -INFINITY : m * kLn2 + logf(l); }
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+// Joins the prefix part's results part, part + parts, ... of a row (the first at at0, the next `rows`
+// further) for columns c0 .. c0 + 7, four at a time.
+__device__ __forceinline__ void merge_prefix(const AttnParams& p, const RequestPlan& rq, int64_t at0, int64_t rows, int c0, bool in,
+                                             int part, int parts, Running& x) {
+  const int D = p.d.d_head;
+  constexpr int kAhead = 4;
+  for (int i0 = part; i0 < rq.n_split; i0 += parts * kAhead) {
+    float z[kAhead], oo[kAhead][8];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * parts;
+      z[u] = i < rq.n_split ? p.part_lse[at0 + i * rows] : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) oo[u][e] = 0.f;
+      if (in && i < rq.n_split) {
+        const float4* y = reinterpret_cast<const float4*>(p.part_o + (at0 + i * rows) * D + c0);
+        const float4 f = y[0], g = y[1];
+        oo[u][0] = f.x; oo[u][1] = f.y; oo[u][2] = f.z; oo[u][3] = f.w;
+        oo[u][4] = g.x; oo[u][5] = g.y; oo[u][6] = g.z; oo[u][7] = g.w;
+      }
+    }
+    float base;
+    x.rescale(fmaxf(fmaxf(fmaxf(x.m, z[0]), fmaxf(z[1], z[2])), z[3]), &base);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const float w = exp2f(z[u] - base);
+      x.l += w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.o[e] = fmaf(w, oo[u][e], x.o[e]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_row(const AttnParams& p, int64_t row, int c0, const Running& x) {
+  const float inv = x.l == 0.f ? 0.f : 1.f / x.l;        // (a NaN score gives a NaN row)
+  T* out = static_cast<T*>(p.out) + row * p.d.d_head + c0;
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(out)[0] = make_float4(x.o[0] * inv, x.o[1] * inv, x.o[2] * inv, x.o[3] * inv);
+    reinterpret_cast<float4*>(out)[1] = make_float4(x.o[4] * inv, x.o[5] * inv, x.o[6] * inv, x.o[7] * inv);
+  } else {
+    *reinterpret_cast<uint4*>(out) = make_uint4(bf16x2(x.o[0] * inv, x.o[1] * inv), bf16x2(x.o[2] * inv, x.o[3] * inv),
+                                                bf16x2(x.o[4] * inv, x.o[5] * inv), bf16x2(x.o[6] * inv, x.o[7] * inv));
+  }
+}
+
+template <typename T, int kLanes>
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ AttnParams p, int parts) {
+  __shared__ float s_ml[kFinishThreads / kLanes][2];
+  __shared__ float s_o[8][kFinishThreads];
+  const int team = threadIdx.x / kLanes, tl = threadIdx.x % kLanes;
+  const int rows_per = kFinishThreads / kLanes / parts, part = team / rows_per;
+  const int64_t row_at = (int64_t)blockIdx.x * rows_per + team % rows_per;
+  const bool live = row_at < p.n_rows;
+  const int64_t row = live ? row_at : p.n_rows - 1;
+  const int D = p.d.d_head, H = p.d.n_head, c0 = tl * 8;
+  const bool in = c0 < D;
+  const int h = (int)(row % H);
+  const int64_t st = row / H, s = st / p.d.L_t;
+  const int t = (int)(st % p.d.L_t), hk = h / (H / p.d.n_kv_head);
+  const RequestPlan& rq = p.req[request_of(p, s)];
+  const float c = p.d.scale * kLog2e;
+  Running x;
+  if (p.d.suffix_cap > 0) {
+    float q[8] = {};
+    if (in) load8(static_cast<const T*>(p.q) + st * p.d.q_token + (int64_t)h * D + c0, q);
+    const int n = visible_suffix(p, s, t);
+    const int per = (n + parts - 1) / parts, end = min(n, (part + 1) * per);
+    const int steps = __reduce_max_sync(0xffffffffu, max(0, end - part * per));    // of the warp's teams
+    const int64_t so = s * p.d.suffix_seq + hk * p.d.suffix_head + c0;
+    const T *k = static_cast<const T*>(p.k_suffix) + so, *v = static_cast<const T*>(p.v_suffix) + so;
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < steps; i0 += kAhead) {
+      float a[kAhead], vv[kAhead][8];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int j = part * per + i0 + u;
+        float kk[8] = {};
+        a[u] = 0.f;
+        if (in && j < end) load8(k + j * p.d.suffix_token, kk);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[u] = fmaf(q[e], kk[e], a[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int j = part * per + i0 + u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vv[u][e] = 0.f;
+        if (in && j < end) load8(v + j * p.d.suffix_token, vv[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+        for (int y = kLanes / 2; y; y >>= 1) a[u] += __shfl_xor_sync(0xffffffffu, a[u], y);
+        a[u] = part * per + i0 + u < end ? a[u] * c : -INFINITY;
+      }
+      float base;
+      x.rescale(fmaxf(fmaxf(fmaxf(x.m, a[0]), fmaxf(a[1], a[2])), a[3]), &base);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float w = exp2f(a[u] - base);
+        x.l += w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x.o[e] = fmaf(w, vv[u][e], x.o[e]);
+      }
+    }
+  }
+  // ---- the prefix part's results
+  cudaGridDependencySynchronize();
+  const int64_t rows = (int64_t)(rq.s1 - rq.s0) * p.d.L_t * H;
+  const int64_t at0 = rq.part + (row - (int64_t)rq.s0 * p.d.L_t * H);
+  merge_prefix(p, rq, at0, rows, c0, in, part, parts, x);
+  if (parts > 1) {
+    if (tl == 0) {
+      s_ml[team][0] = x.m;
+      s_ml[team][1] = x.l;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_o[e][threadIdx.x] = x.o[e];
+    __syncthreads();
+    if (part > 0) return;
+    for (int i = 1; i < parts; ++i) {
+      const int other = team + i * rows_per;
+      float base;
+      const float m = s_ml[other][0];
+      x.rescale(fmaxf(x.m, m), &base);
+      const float w = exp2f(m - base);
+      x.l = fmaf(w, s_ml[other][1], x.l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.o[e] = fmaf(w, s_o[e][other * kLanes + tl], x.o[e]);
+    }
+  }
+  if (!live) return;
+  if (in) store_row<T>(p, row, c0, x);
+  if (p.lse && tl == 0) p.lse[row] = x.lse();
+}
+
+template <typename T, int kLanes>
+tr_status launch_finish(const AttnParams& p, int sms, cudaStream_t st) {
+  // several teams per row while there are few rows and enough to share: about 16 warps per SM
+  int parts = 1, items = p.d.suffix_cap;
+  for (int r = 0; r < p.R; ++r) items = std::max(items, p.req[r].n_split);
+  while (parts < 16 && parts * 2 <= kFinishThreads / kLanes && items > 4 * parts &&
+         p.n_rows * kLanes * parts * 2 <= (int64_t)sms * 16 * 32)
+    parts *= 2;
+  const int rows_per = kFinishThreads / kLanes / parts;
+  return launch_dependent(finish_kernel<T, kLanes>, (unsigned)((p.n_rows + rows_per - 1) / rows_per), kFinishThreads, 0, st,
+                          "finish_kernel", p, parts);
+}
+template <typename T>
+tr_status launch_finish(const AttnParams& p, int sms, cudaStream_t st) {
+  const int D = p.d.d_head;
+  return D <= 8    ? launch_finish<T, 1>(p, sms, st)
+         : D <= 16 ? launch_finish<T, 2>(p, sms, st)
+         : D <= 32 ? launch_finish<T, 4>(p, sms, st)
+         : D <= 64 ? launch_finish<T, 8>(p, sms, st)
+                   : launch_finish<T, 16>(p, sms, st);
+}
+
+// The same for bf16 suffixes of eight tokens and more, on warp-level matrix instructions: the L_t x
+// (n_head / n_kv_head) rows of a sequence that share a key head are one 16-row operand against
+// 16 of its keys at a time, so each key and value is read once for all of them, straight into the
+// fragments of the products (the order of d_head within a product is free, so a lane's 16 bytes
+// of a key are its share of two slices; of values, of eight column tiles).  `parts` warps share a
+// sequence's keys; all meet in shared memory, where the prefix part's results join.
+constexpr int kSuffixThreads = 128;
+
+__device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int kBlocks>     // 64-wide blocks of d_head
+__global__ void __launch_bounds__(kSuffixThreads) suffix_kernel(const __grid_constant__ AttnParams p, int parts, int m_tiles) {
+  constexpr int DP = kBlocks * 64;
+  __shared__ float s_o[kSuffixThreads / 32][16][DP + 4], s_m[kSuffixThreads / 32][16], s_l[kSuffixThreads / 32][16];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4;
+  const int units = kSuffixThreads / 32 / parts, part = warp % parts, D = p.d.d_head, H = p.d.n_head, Hk = p.d.n_kv_head;
+  const int G = H / Hk, n_rows = p.d.L_t * G;
+  const int64_t n_unit = (int64_t)p.req[p.R].s0 * Hk * m_tiles;
+  const int64_t u_at = (int64_t)blockIdx.x * units + warp / parts, u = min(u_at, n_unit - 1);
+  const int mt = (int)(u % m_tiles), hk = (int)(u / m_tiles % Hk);
+  const int64_t s = u / m_tiles / Hk;
+  const int row0 = mt * 16;                               // of the sequence's rows of this key head: t * G + head in group
+  const float c = p.d.scale * kLog2e;
+  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  // ---- Q: 16 bytes of rows g and g + 8 per 32 columns
+  uint4 q[2][2 * kBlocks];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = row0 + g + 8 * h;
+    const __nv_bfloat16* src = qp + (s * p.d.L_t + r / G) * p.d.q_token + (int64_t)(hk * G + r % G) * D;
+#pragma unroll
+    for (int i = 0; i < 2 * kBlocks; ++i)
+      q[h][i] = r < n_rows && i * 32 + qd * 8 < D ? __ldg(reinterpret_cast<const uint4*>(src + i * 32 + qd * 8)) : zero;
+  }
+  // keys seen by rows g, g + 8 and, at most, by any row of the sequence
+  const int t0 = min((row0 + g) / G, p.d.L_t - 1), t1 = min((row0 + g + 8) / G, p.d.L_t - 1);
+  const int n0 = visible_suffix(p, s, t0), n1 = visible_suffix(p, s, t1), n = visible_suffix(p, s, p.d.L_t - 1);
+  const int64_t so = s * p.d.suffix_seq + hk * p.d.suffix_head;
+  const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(p.k_suffix) + so, *vp = static_cast<const __nv_bfloat16*>(p.v_suffix) + so;
+  float o[8 * kBlocks][4] = {};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  for (int j0 = part * 16; j0 < n; j0 += parts * 16) {
+    uint4 k[2][2 * kBlocks], v[4][kBlocks];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = j0 + g + 8 * h;
+#pragma unroll
+      for (int i = 0; i < 2 * kBlocks; ++i)
+        k[h][i] = j < n && i * 32 + qd * 8 < D ? __ldg(reinterpret_cast<const uint4*>(kp + j * p.d.suffix_token + i * 32 + qd * 8)) : zero;
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int j = j0 + 2 * qd + (h & 1) + (h >> 1) * 8;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+        v[h][b] = j < n && b * 64 + g * 8 < D ? __ldg(reinterpret_cast<const uint4*>(vp + j * p.d.suffix_token + b * 64 + g * 8)) : zero;
+    }
+    float sc[2][4] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2 * kBlocks; ++i) {
+        const uint32_t a0[4] = {q[0][i].x, q[1][i].x, q[0][i].y, q[1][i].y}, a1[4] = {q[0][i].z, q[1][i].z, q[0][i].w, q[1][i].w};
+        mma_16816(sc[h], a0, k[h][i].x, k[h][i].y);
+        mma_16816(sc[h], a1, k[h][i].z, k[h][i].w);
+      }
+    // rows g (r = 0) and g + 8 (r = 1); columns 2 qd, 2 qd + 1 of each key tile h
+    uint32_t w[2][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int seen = r ? n1 : n0;
+      float a[4], top = m[r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + (e >> 1) * 8 + 2 * qd + (e & 1);
+        a[e] = j < seen ? sc[e >> 1][2 * r + (e & 1)] * c : -INFINITY;
+        top = fmaxf(top, a[e]);
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float base = top == -INFINITY ? 0.f : top, f = exp2f(m[r] - base);
+      m[r] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = exp2f(a[e] - base);
+        sum += a[e];
+      }
+      l[r] = l[r] * f + sum;
+      w[r][0] = bf16x2(a[0], a[1]);
+      w[r][1] = bf16x2(a[2], a[3]);
+#pragma unroll
+      for (int i = 0; i < 8 * kBlocks; ++i) {
+        o[i][2 * r] *= f;
+        o[i][2 * r + 1] *= f;
+      }
+    }
+    const uint32_t a[4] = {w[0][0], w[1][0], w[0][1], w[1][1]};
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t x[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) x[h] = (&v[h][b].x)[i / 2];
+        const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
+        mma_16816(o[b * 8 + i], a, __byte_perm(x[0], x[1], sel), __byte_perm(x[2], x[3], sel));
+      }
+  }
+  // ---- rows g, g + 8: columns b * 64 + 16 qd + i (and + 8 + i) of column tile (b, i)
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    if (qd == 0) {
+      s_m[warp][g + 8 * r] = m[r];
+      s_l[warp][g + 8 * r] = l[r];
+    }
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        float* d = &s_o[warp][g + 8 * r][b * 64 + 16 * qd + i];
+        *reinterpret_cast<float4*>(d) = make_float4(o[b * 8 + i][2 * r], o[b * 8 + i + 1][2 * r], o[b * 8 + i + 2][2 * r], o[b * 8 + i + 3][2 * r]);
+        *reinterpret_cast<float4*>(d + 8) = make_float4(o[b * 8 + i][2 * r + 1], o[b * 8 + i + 1][2 * r + 1], o[b * 8 + i + 2][2 * r + 1],
+                                                        o[b * 8 + i + 3][2 * r + 1]);
+      }
+  }
+  cudaGridDependencySynchronize();
+  __syncthreads();
+  // ---- eight columns of a row per thread: the warps' results, then the prefix part's
+  if (u_at >= n_unit) return;
+  const RequestPlan& rq = p.req[request_of(p, s)];
+  const int64_t rows = (int64_t)(rq.s1 - rq.s0) * p.d.L_t * H;
+  const int chunks = D / 8, first = warp / parts * parts;
+  for (int item = part * 32 + lane; item < min(16, n_rows - row0) * chunks; item += parts * 32) {
+    const int rr = item / chunks, c0 = item % chunks * 8, r = row0 + rr;
+    const int64_t row = (s * p.d.L_t + r / G) * H + hk * G + r % G;
+    Running x;
+    for (int i = 0; i < parts; ++i) {
+      const float mm = s_m[first + i][rr];
+      float base;
+      x.rescale(fmaxf(x.m, mm), &base);
+      const float f = exp2f(mm - base);
+      x.l = fmaf(f, s_l[first + i][rr], x.l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.o[e] = fmaf(f, s_o[first + i][rr][c0 + e], x.o[e]);
+    }
+    merge_prefix(p, rq, rq.part + (row - (int64_t)rq.s0 * p.d.L_t * H), rows, c0, true, 0, 1, x);
+    store_row<__nv_bfloat16>(p, row, c0, x);
+    if (p.lse && c0 == 0) p.lse[row] = x.lse();
+  }
+}
+
+template <int kBlocks>
+tr_status launch_suffix(const AttnParams& p, cudaStream_t st) {
+  // a warp per 16 keys up to the four of a CTA
+  const int steps = (p.d.suffix_cap + 15) / 16, parts = steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
+  const int m_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 15) / 16, units = kSuffixThreads / 32 / parts;
+  const int64_t n_unit = (int64_t)p.req[p.R].s0 * p.d.n_kv_head * m_tiles;
+  return launch_dependent(suffix_kernel<kBlocks>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
+                          parts, m_tiles);
 }
 
 tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t* prefix, int R) {
@@ -218,6 +561,7 @@ void plan_units(AttnParams& p, int sms) {
 struct Plan {
   bool direct = false;        // the tensor-core kernel writes the results
   size_t bytes = 0;
+  int sms = 0;
 };
 tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* prefix, int R, AttnParams& p, Plan& plan) {
   TR_TRY(check_offsets(d, seq, prefix, R));
@@ -232,12 +576,10 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
     q.p1 = (int)prefix[std::min(r + 1, R)];
   }
   p.n_units = 0;
+  TR_TRY(sm_count(&plan.sms));
   if (d->dtype != TR_BF16) return TR_OK;
-  int dev = 0, sms = 0;
-  TR_CUDA_TRY(cudaGetDevice(&dev));
-  TR_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  plan_units(p, sms);
-  plan.direct = d->suffix_cap == 0;
+  plan_units(p, plan.sms);
+  plan.direct = d->suffix_cap <= kDirectSuffix;
   for (int r = 0; r < R; ++r) plan.direct = plan.direct && (p.req[r].n_split == 1 || p.req[r].s0 == p.req[r].s1);
   if (!plan.direct) plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);
   return TR_OK;
@@ -294,11 +636,12 @@ extern "C" tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q
   p.part_lse = p.part_o + p.req[R].part * desc->d_head;
   if (p.n_units > 0) TR_TRY(launch_prefix_tc(p, plan.direct, st));
   if (plan.direct) return TR_OK;
+  if (desc->dtype == TR_BF16) {
+    if (desc->suffix_cap >= 8) return desc->d_head <= 64 ? launch_suffix<1>(p, st) : launch_suffix<2>(p, st);
+    return launch_finish<__nv_bfloat16>(p, plan.sms, st);
+  }
   const unsigned grid = (unsigned)((p.n_rows + kRowWarps - 1) / kRowWarps);
-  if (desc->dtype == TR_F32)
-    attn_row_kernel<float, false><<<grid, kRowWarps * 32, 0, st>>>(p);
-  else
-    attn_row_kernel<__nv_bfloat16, true><<<grid, kRowWarps * 32, 0, st>>>(p);
+  attn_row_kernel<float><<<grid, kRowWarps * 32, 0, st>>>(p);
   TR_LAUNCH_CHECK("attn_row_kernel");
   return TR_OK;
 }

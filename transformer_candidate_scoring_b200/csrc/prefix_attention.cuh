@@ -44,8 +44,21 @@ __host__ __device__ inline int64_t request_rows(const AttnParams& p, int r) {
   return (int64_t)(p.req[r].s1 - p.req[r].s0) * p.d.L_t * p.d.n_head;
 }
 
-// Launches the tensor-core kernel over every unit of the plan (bf16).  With `direct`, each row
-// has one partial result and no suffix: out and lse are written instead of it.
+// Suffix keys that query token t of sequence s sees; a length outside the buffer is clamped.
+__device__ __forceinline__ int visible_suffix(const AttnParams& p, int64_t s, int t) {
+  if (p.d.suffix_cap == 0) return 0;
+  int len = p.suffix_len[s];
+  if (len < 0 || len > p.d.suffix_cap) {
+    atomicOr(p.status, STATUS_KEY_RANGE);
+    len = min(max(len, 0), p.d.suffix_cap);
+  }
+  return p.d.causal ? max(0, len - (p.d.L_t - 1 - t)) : len;
+}
+
+// Launches the tensor-core kernel over every unit of the plan (bf16).  With `direct`, every row
+// has exactly one partial result and suffix buffers hold at most kDirectSuffix tokens: the kernel adds
+// the row's own keys and writes out and lse instead.
+constexpr int kDirectSuffix = 4;
 tr_status launch_prefix_tc(const AttnParams& p, bool direct, cudaStream_t st);
 
 }  // namespace attn

@@ -101,6 +101,12 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
+// acc + the products of two bf16 pairs.
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
+  acc = fmaf(__uint_as_float(a << 16), __uint_as_float(b << 16), acc);
+  return fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u), acc);
+}
+
 struct Bars {
   uint32_t kfull, kempty, vfull, vempty;   // rings, 8 bytes apart
   uint32_t qfull, sfull, pfull, odone;     // per tile
@@ -386,9 +392,50 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
     tc_fence_after();
     const bool second = !x.two && x.steps > 1;               // tile 1 has an O
     if (warp_live) {
-      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-      const float lse2 = lsum == 0.f ? -INFINITY : __fmul_rn(mref, c) + log2f(lsum);
       const int64_t row = token * p.d.n_head + head;
+      // ---- with `direct`, the row's own few keys join here: their scores from the Q row in shared
+      // memory, their values beside O below
+      const int64_t seq = token / p.d.L_t;
+      const int64_t own = seq * p.d.suffix_seq + (int64_t)x.hk * p.d.suffix_head;
+      float a[kDirectSuffix], ref = __fmul_rn(mref, c);
+      int n_own = 0, n_warp = 0;
+      if (tp.direct && p.d.suffix_cap > 0) {
+        n_own = live ? visible_suffix(p, seq, (int)(token % p.d.L_t)) : 0;
+        n_warp = __reduce_max_sync(0xffffffffu, n_own);
+        float top = ref;
+#pragma unroll
+        for (int j = 0; j < kDirectSuffix; ++j) {
+          a[j] = -INFINITY;
+          if (j < n_own) {
+            const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_suffix) + own + j * p.d.suffix_token);
+            const uint32_t qr = smem + L::Q + t * L::TILE + tid * 128;
+            float acc = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 kv = __ldg(kr + i);
+              uint4 qv;
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(qv.x), "=r"(qv.y), "=r"(qv.z), "=r"(qv.w)
+                           : "r"(qr + (i >> 3) * (128 * 128) + (((i & 7) ^ (tid & 7)) << 4)));
+              acc = dot2(qv.x, kv.x, dot2(qv.y, kv.y, dot2(qv.z, kv.z, dot2(qv.w, kv.w, acc))));
+            }
+            a[j] = acc * c;
+            top = fmaxf(top, a[j]);
+          }
+        }
+        const float tb = top == -INFINITY ? 0.f : top, f = ref == top ? 1.f : ex2(ref - tb);
+        lsum *= f;
+        w0 *= f;
+        w1 *= f;
+#pragma unroll
+        for (int j = 0; j < kDirectSuffix; ++j) {
+          a[j] = ex2(a[j] - tb);
+          lsum += a[j];
+        }
+        ref = top;
+      }
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+      const float lse2 = lsum == 0.f ? -INFINITY : ref + log2f(lsum);
       const int64_t part = rq.part + x.split * request_rows(p, x.r) + (row - (int64_t)rq.s0 * p.d.L_t * p.d.n_head);
       for (int i = 0; i * 16 < D; ++i) {
         float o[16], o1[16];
@@ -398,7 +445,25 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
         reg_fence<16>(o);
         reg_fence<16>(o1);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = (second ? o[e] * w0 + o1[e] * w1 : o[e] * w0) * inv;
+        for (int e = 0; e < 16; ++e) o[e] = second ? o[e] * w0 + o1[e] * w1 : o[e] * w0;
+#pragma unroll
+        for (int j = 0; j < kDirectSuffix; ++j)
+          if (j < n_warp) {
+            const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_suffix) + own + j * p.d.suffix_token) + 2 * i;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (j < n_own && 16 * i + 8 * h < D) {
+                const uint4 v = __ldg(vr + h);
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  o[8 * h + 2 * e] = fmaf(a[j], __uint_as_float(vw[e] << 16), o[8 * h + 2 * e]);
+                  o[8 * h + 2 * e + 1] = fmaf(a[j], __uint_as_float(vw[e] & 0xFFFF0000u), o[8 * h + 2 * e + 1]);
+                }
+              }
+          }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] *= inv;
         if (live) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -465,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  cudaTriggerProgrammaticLaunchCompletion();   // the merge kernel's own part may start where SMs fall idle
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
     if (warp == 8 && lane == 0) load_steps<DH>(p.a, &p.kmap, smem + L::K, L::NK, b.kfull, b.kempty, abort_flag);
@@ -532,9 +598,8 @@ tr_status launch_prefix_tc(const AttnParams& a, bool direct, cudaStream_t st) {
   p.direct = direct;
   TR_TRY(encode_map(&p.kmap, a.k_prefix, a));
   TR_TRY(encode_map(&p.vmap, a.v_prefix, a));
-  int dev = 0, sms = 0;
-  TR_CUDA_TRY(cudaGetDevice(&dev));
-  TR_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  int sms = 0;
+  TR_TRY(sm_count(&sms));
   return a.d.d_head <= 64 ? launch<64>(p, sms, st) : launch<128>(p, sms, st);
 }
 
