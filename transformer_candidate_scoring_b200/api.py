@@ -6,6 +6,9 @@ CUDA stream; every step of the computation runs in libtr's kernels.
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import math
+import struct
 from typing import Dict, Sequence
 
 import numpy as np
@@ -245,23 +248,35 @@ def topk(scores: torch.Tensor, req_offsets: Sequence[int], k: int, out_idx: torc
     return out_idx, out_score
 
 
-def _on(stream, *tensors):
-    """The device all of ``tensors`` (None aside) are on, and the stream to launch on: ``stream``,
-    or that device's current one."""
-    dev = None
+def _on(*tensors) -> int:
+    """The device ordinal that all of ``tensors`` (None aside) are on."""
+    dev = -1
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    return dev, _stream(torch.cuda.current_stream(dev) if stream is None else stream)
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("expected CUDA tensors")
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError(f"tensors on different devices: cuda:{dev} and cuda:{d}")
+                dev = d
+    return dev
 
 
-def _new(shape, dtype, dev, stream) -> torch.Tensor:
+def _run(dev: int, stream, call, *args) -> None:
+    """call(*args, stream) with ``dev`` current, on ``stream`` or that device's current one."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == dev:
+        _check(call(*args, raw))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(*args, raw))
+
+
+def _new(shape, dtype, dev: int, stream) -> torch.Tensor:
     """A buffer from torch's allocator for work on ``stream`` (None: the current one), kept from
     reuse until that work is done."""
     t = torch.empty(shape, dtype=dtype, device=dev)
@@ -270,38 +285,76 @@ def _new(shape, dtype, dev, stream) -> torch.Tensor:
     return t
 
 
-def _workspace(workspace, need: int, dev, stream):
-    """``workspace`` if it is large enough, or a new buffer of ``need`` bytes."""
-    if workspace is not None:
-        if not workspace.is_contiguous() or workspace.device != dev:
-            raise ValueError("workspace: expected a contiguous tensor on the inputs' device")
-        size = workspace.numel() * workspace.element_size()
-        if size < need:
-            raise ValueError(f"workspace of {size} bytes: need {need}")
-        return workspace, size
-    return _new((max(need, 16),), torch.uint8, dev, stream), need
+def _workspace(workspace, need: int, dev: int, stream):
+    """``workspace`` if it is large enough, or a new buffer of ``need`` bytes; and its size."""
+    if workspace is None:
+        return _new((max(need, 16),), torch.uint8, dev, stream), need
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace: expected a contiguous tensor on the inputs' device")
+    size = workspace.numel() * workspace.element_size()
+    if size < need:
+        raise ValueError(f"workspace of {size} bytes: need {need}")
+    return workspace, size
 
 
-def _host_offsets(x, what: str):
-    a = [int(v) for v in x]
-    if len(a) < 2:
-        raise ValueError(f"{what}: expected R + 1 offsets")
-    return (C.c_int64 * len(a))(*a), a
+def _layout(t):
+    """What a call's checks and strides depend on; None for no tensor."""
+    return None if t is None else (t.shape, t.stride(), t.dtype)
 
 
 def _kv_strides(k, v, what: str):
-    """The strides of a key and a value tensor whose rows of d_head are contiguous."""
-    if k.shape != v.shape or k.dtype != v.dtype:
+    """The strides of keys and values (layouts) whose rows of d_head are contiguous."""
+    (shape, stride, dtype), empty = k, 0 in k[0]
+    if v[0] != shape or v[2] != dtype:
         raise ValueError(f"{what}: keys and values differ in shape or type")
-    if k.stride() != v.stride() and k.numel() > 0:
+    if not empty and v[1] != stride:
         raise ValueError(f"{what}: keys and values differ in strides")
-    if k.numel() > 0 and k.shape[-1] > 1 and k.stride(-1) != 1:
+    if not empty and shape[-1] > 1 and stride[-1] != 1:
         raise ValueError(f"{what}: the head dimension must be contiguous")
     # a dimension of one entry may come with any stride; it is never multiplied
-    inner, strides = k.shape[-1], []
-    for size, stride in zip(reversed(k.shape[:-1]), reversed(k.stride()[:-1])):
-        strides.insert(0, stride if size > 1 else max(inner, 1))
-    return strides
+    return [st if n > 1 else max(shape[-1], 1) for n, st in zip(shape[:-1], stride[:-1])]
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_plan(q, kp, vp, ks, vs, sl, po, so, scale, causal, dev):
+    """The checked arguments of a prefix_attention call that follow from its layouts and offsets, and the
+    bytes of its workspace."""
+    shape, stride, dtype = q
+    if len(shape) not in (3, 4) or len(kp[0]) != 3:
+        raise ValueError("expected q [n, L_t, H, d] or [n, H, d] and k_prefix, v_prefix [T, H_kv, d]")
+    n, H, d = shape[0], shape[-2], shape[-1]
+    L_t = shape[1] if len(shape) == 4 else 1
+    H_kv = kp[0][1]
+    if 0 not in shape and ((d > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != d)):
+        raise ValueError("q: the heads of a token must be contiguous")
+    q_token = H * d if n <= 1 and L_t == 1 else stride[0] if L_t == 1 else stride[1]
+    if L_t > 1 and n > 1 and stride[0] != L_t * stride[1]:
+        raise ValueError("q: the tokens must follow one another at one stride")
+    pk = _kv_strides(kp, vp, "prefix")
+    if kp[0][2] != d or kp[2] != dtype:
+        raise ValueError("prefix: head width or type differs from q's")
+    if len(po) < 2 or len(po) != len(so):
+        raise ValueError("expected R + 1 prefix_offsets and as many seq_offsets")
+    if so[-1] != n or po[-1] > kp[0][0]:
+        raise ValueError("seq_offsets must end at n, prefix_offsets within k_prefix")
+    S, sk = 0, (0, 0, 0)
+    if (ks is None) != (vs is None) or (ks is None) != (sl is None):
+        raise ValueError("k_suffix, v_suffix and suffix_len come together")
+    if ks is not None:
+        if len(ks[0]) != 4 or ks[0][0] != n or ks[0][2:] != (H_kv, d) or ks[2] != dtype:
+            raise ValueError("expected k_suffix, v_suffix [n, S, H_kv, d] of q's type")
+        if sl[2] != torch.int32 or sl[0] != (n,) or (n > 1 and sl[1] != (1,)):
+            raise ValueError("suffix_len: expected contiguous int32 [n]")
+        S, sk = ks[0][1], _kv_strides(ks, vs, "suffix")
+    desc = L.AttnDesc(H, H_kv, d, L_t, int(causal), S, d ** -0.5 if scale is None else scale, dtype_code(dtype), q_token,
+                      pk[0], pk[1], sk[0], sk[1], sk[2])
+    R = len(so) - 1
+    so_c, po_c = (C.c_int64 * (R + 1))(*so), (C.c_int64 * (R + 1))(*po)
+    with torch.cuda.device(dev):
+        need = L.load().tr_prefix_attention_workspace(C.byref(desc), so_c, po_c, R)
+    if need == C.c_size_t(-1).value:
+        _check(L.TR_ERR_INVALID_ARG)
+    return C.pointer(desc), so_c, po_c, R, S, need
 
 
 def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, prefix_offsets: Sequence[int],
@@ -317,42 +370,10 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     the first suffix_len[s] (int32) tokens of their own k_suffix, v_suffix [n, S, H_kv, d];
     with ``causal``, query token t to L_t - 1 - t fewer of those.  ``scale`` defaults to
     1 / sqrt(d).  bf16 or fp32.  Buffers that are not given are allocated."""
-    dev, st = _on(stream, q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_len, out, lse)
-    if q.dim() not in (3, 4) or k_prefix.dim() != 3:
-        raise ValueError("expected q [n, L_t, H, d] or [n, H, d] and k_prefix, v_prefix [T, H_kv, d]")
-    n, H, d = q.shape[0], q.shape[-2], q.shape[-1]
-    L_t = q.shape[1] if q.dim() == 4 else 1
-    H_kv = k_prefix.shape[1]
-    if q.numel() and ((d > 1 and q.stride(-1) != 1) or (H > 1 and q.stride(-2) != d)):
-        raise ValueError("q: the heads of a token must be contiguous")
-    q_token = q.stride(-3)
-    if q.dim() == 4:
-        if L_t == 1:
-            q_token = q.stride(0)
-        elif n > 1 and q.stride(0) != L_t * q.stride(1):
-            raise ValueError("q: the tokens must follow one another at one stride")
-    if n <= 1 and L_t == 1:
-        q_token = H * d
-    pk = _kv_strides(k_prefix, v_prefix, "prefix")
-    if k_prefix.shape[2] != d or k_prefix.dtype != q.dtype:
-        raise ValueError("prefix: head width or type differs from q's")
-    po, po_list = _host_offsets(prefix_offsets, "prefix_offsets")
-    so, so_list = _host_offsets(seq_offsets, "seq_offsets")
-    if len(po_list) != len(so_list):
-        raise ValueError("prefix_offsets and seq_offsets differ in length")
-    if so_list[-1] != n or po_list[-1] > k_prefix.shape[0]:
-        raise ValueError("seq_offsets must end at n, prefix_offsets within k_prefix")
-    S, sk = 0, (0, 0, 0)
-    if k_suffix is not None:
-        if v_suffix is None or suffix_len is None:
-            raise ValueError("k_suffix, v_suffix and suffix_len come together")
-        if k_suffix.dim() != 4 or k_suffix.shape[0] != n or k_suffix.shape[2:] != (H_kv, d) or k_suffix.dtype != q.dtype:
-            raise ValueError("expected k_suffix, v_suffix [n, S, H_kv, d] of q's type")
-        if suffix_len.dtype != torch.int32 or suffix_len.shape != (n,) or not suffix_len.is_contiguous():
-            raise ValueError("suffix_len: expected contiguous int32 [n]")
-        S, sk = k_suffix.shape[1], _kv_strides(k_suffix, v_suffix, "suffix")
-    elif v_suffix is not None or suffix_len is not None:
-        raise ValueError("k_suffix, v_suffix and suffix_len come together")
+    dev = _on(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_len, out, lse)
+    desc, so, po, R, S, need = _attention_plan(
+        _layout(q), _layout(k_prefix), _layout(v_prefix), _layout(k_suffix), _layout(v_suffix), _layout(suffix_len),
+        tuple(map(int, prefix_offsets)), tuple(map(int, seq_offsets)), None if scale is None else float(scale), bool(causal), dev)
     if out is None:
         out = _new(q.shape, q.dtype, dev, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
@@ -361,19 +382,38 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
         lse = _new(q.shape[:-1], torch.float32, dev, stream)
     elif lse.shape != q.shape[:-1] or lse.dtype != torch.float32:
         raise ValueError("lse: expected fp32 of q's shape without the last dimension")
-    desc = L.AttnDesc(H, H_kv, d, L_t, int(bool(causal)), S, d ** -0.5 if scale is None else float(scale),
-                      dtype_code(q.dtype), q_token, pk[0], pk[1], sk[0], sk[1], sk[2])
-    lib, R = L.load(), len(so_list) - 1
-    with torch.cuda.device(dev):
-        need = lib.tr_prefix_attention_workspace(C.byref(desc), so, po, R)
-        if need == C.c_size_t(-1).value:
-            _check(L.TR_ERR_INVALID_ARG)
-        ws, size = _workspace(workspace, need, dev, stream)
-        _check(lib.tr_prefix_attention(
-            C.byref(desc), q.data_ptr(), so, k_prefix.data_ptr(), v_prefix.data_ptr(), po,
-            k_suffix.data_ptr() if S else None, v_suffix.data_ptr() if S else None,
-            suffix_len.data_ptr() if S else None, R, _ptr(out), _ptr(lse), ws.data_ptr(), size, st))
+    ws, size = _workspace(workspace, need, dev, stream)
+    _run(dev, stream, L.load().tr_prefix_attention, desc, q.data_ptr(), so, k_prefix.data_ptr(), v_prefix.data_ptr(), po,
+         k_suffix.data_ptr() if S else None, v_suffix.data_ptr() if S else None, suffix_len.data_ptr() if S else None, R,
+         _ptr(out), _ptr(lse), ws.data_ptr(), size)
     return out, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def _select_plan(logits, cum, finished, allowed, k):
+    """The checked arguments of a beam_select call that follow from its layouts, and the bytes of
+    its workspace."""
+    if len(cum[0]) != 2 or cum[2] != torch.float32:
+        raise ValueError("cum: expected fp32 [R, W]")
+    R, W = cum[0]
+    shape, stride, dtype = logits
+    V = shape[-1]
+    if len(shape) == 3 and shape[:2] == (R, W) and (R <= 1 or W <= 1 or stride[0] == W * stride[1]):
+        shape, stride = (R * W, V), (stride[1] if W > 1 else stride[0], stride[2])
+    if len(shape) != 2 or shape[0] != R * W or (V > 1 and stride[1] != 1):
+        raise ValueError("logits: expected [R*W, V] or [R, W, V], contiguous along V, rows at one stride")
+    if finished is not None and (finished[2] not in (torch.bool, torch.uint8) or math.prod(finished[0]) != R * W):
+        raise ValueError("finished: expected bool or uint8 [R, W]")
+    if allowed is not None:
+        (ash, ast, adt), words = allowed, -(-V // 32)
+        if adt != torch.int32 or len(ash) != 2 or ash[0] != R * W or (ash[1] > 1 and ast[1] != 1) or ash[1] < words:
+            raise ValueError("allowed: expected int32 [R*W, ceil(V/32)], contiguous along the words")
+    need = L.load().tr_beam_select_workspace(R, W, V, k)
+    if need == C.c_size_t(-1).value:
+        _check(L.TR_ERR_INVALID_ARG)
+    one = R * W <= 1
+    return (dtype_code(dtype), V if one else stride[0], 0 if allowed is None else allowed[0][1] if one else allowed[1][0], R, W, V,
+            need)
 
 
 def beam_select(logits: torch.Tensor, cum: torch.Tensor, k: int, *, finished: torch.Tensor = None,
@@ -385,47 +425,36 @@ def beam_select(logits: torch.Tensor, cum: torch.Tensor, k: int, *, finished: to
     int32 [R, k], token int32 [R, k], score fp32 [R, k]), best first.  ``finished`` bool or uint8
     [R, W]; ``allowed`` int32 [R*W, ceil(V/32)] or more words: bit v % 32 of word v // 32 allows
     token v."""
-    dev, st = _on(stream, logits, cum, finished, allowed, parent, token, score)
-    if cum.dim() != 2 or cum.dtype != torch.float32:
-        raise ValueError("cum: expected fp32 [R, W]")
-    R, W = cum.shape
-    V = logits.shape[-1]
-    rows = logits.view(R * W, V) if logits.dim() == 3 else logits
-    if rows.dim() != 2 or rows.shape[0] != R * W or (V > 1 and rows.stride(1) != 1):
-        raise ValueError("logits: expected [R*W, V] or [R, W, V], contiguous along V")
-    if finished is not None and (finished.dtype not in (torch.bool, torch.uint8) or finished.numel() != R * W):
-        raise ValueError("finished: expected bool or uint8 [R, W]")
-    if allowed is not None and (allowed.dtype != torch.int32 or allowed.dim() != 2 or allowed.shape[0] != R * W
-                                or (allowed.shape[1] > 1 and allowed.stride(1) != 1) or allowed.shape[1] * 32 < V):
-        raise ValueError("allowed: expected int32 [R*W, ceil(V/32)], contiguous along the words")
+    dev = _on(logits, cum, finished, allowed, parent, token, score)
+    k = int(k)
+    code, ld, allowed_ld, R, W, V, need = _select_plan(_layout(logits), _layout(cum), _layout(finished), _layout(allowed), k)
     for name, t, dt in (("parent", parent, torch.int32), ("token", token, torch.int32), ("score", score, torch.float32)):
         if t is not None and (t.shape != (R, k) or t.dtype != dt):
             raise ValueError(f"{name}: expected {dt} [R, k]")
-    lib = L.load()
-    need = lib.tr_beam_select_workspace(R, W, V, int(k))
-    if need == C.c_size_t(-1).value:
-        _check(L.TR_ERR_INVALID_ARG)
     if parent is None:
         parent = _new((R, k), torch.int32, dev, stream)
     if token is None:
         token = _new((R, k), torch.int32, dev, stream)
     if score is None:
         score = _new((R, k), torch.float32, dev, stream)
-    with torch.cuda.device(dev):
-        ws, size = _workspace(workspace, need, dev, stream)
-        _check(lib.tr_beam_select(
-            rows.data_ptr(), dtype_code(rows.dtype), rows.stride(0) if R * W > 1 else V, _ptr(cum), _ptr(finished),
-            None if allowed is None else allowed.data_ptr(),
-            0 if allowed is None else allowed.stride(0) if R * W > 1 else allowed.shape[1],
-            R, W, V, int(k), int(pad_token), _ptr(parent), _ptr(token), _ptr(score), ws.data_ptr(), size, st))
+    ws, size = _workspace(workspace, need, dev, stream)
+    _run(dev, stream, L.load().tr_beam_select, logits.data_ptr(), code, ld, _ptr(cum), _ptr(finished),
+         None if allowed is None else allowed.data_ptr(), allowed_ld, R, W, V, k, int(pad_token), _ptr(parent), _ptr(token),
+         _ptr(score), ws.data_ptr(), size)
     return parent, token, score
 
 
-def _row_bytes(t: torch.Tensor) -> int:
-    """Bytes of one row of t, whose elements must be contiguous within the row."""
-    if t.dim() < 1 or (t.numel() and not t[0].is_contiguous()):
-        raise ValueError("states: the elements of a row must be contiguous")
-    return t[0].numel() * t.element_size() if t.shape[0] else 0
+@functools.lru_cache(maxsize=1024)
+def _row_layout(shape, stride, size: int):
+    """(rows, bytes from row to row, bytes of a row) of a tensor whose rows are contiguous."""
+    if len(shape) < 1:
+        raise ValueError("states: expected rows")
+    inner = 1
+    for n, st in zip(reversed(shape[1:]), reversed(stride[1:])):
+        if n > 1 and st != inner and 0 not in shape:
+            raise ValueError("states: the elements of a row must be contiguous")
+        inner *= n
+    return shape[0], (stride[0] if shape[0] > 1 else inner) * size, inner * size
 
 
 def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor, outs: Sequence[torch.Tensor] = None,
@@ -436,29 +465,33 @@ def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor, outs: Seq
     else into outs [R*W_out, ...].  Any number of states."""
     states = list(states)
     dsts = states if outs is None else list(outs)
-    dev, st = _on(stream, parent, *states, *dsts)
     if parent.dim() != 2 or parent.dtype != torch.int32:
         raise ValueError("parent: expected int32 [R, W_out]")
     R, W_out = parent.shape
     if len(dsts) != len(states):
         raise ValueError("outs: expected one per state")
+    dev = _on(parent, *states) if outs is None else _on(parent, *states, *dsts)
     if not states or not R:
         return dsts
     W_in = states[0].shape[0] // R
-    arr = (L.BeamState * len(states))()
+    flat = []
     for i, (s, o) in enumerate(zip(states, dsts)):
-        if s.shape[0] != R * W_in or o.shape != (R * W_out, *s.shape[1:]) or o.dtype != s.dtype:
-            raise ValueError(f"state {i}: expected rows [R*W_in, ...] and an out [R*W_out, ...] of the same type")
-        nb = _row_bytes(s)
-        _row_bytes(o)
-        e = s.element_size()
-        arr[i] = L.BeamState(o.data_ptr(), s.data_ptr(), o.stride(0) * e if R * W_out > 1 else nb,
-                             s.stride(0) * e if R * W_in > 1 else nb, nb)
-    lib = L.load()
-    with torch.cuda.device(dev):
-        for i in range(0, len(states), L.TR_MAX_STATES):
-            m = min(L.TR_MAX_STATES, len(states) - i)
-            _check(lib.tr_beam_reorder(C.pointer(arr[i]), m, _ptr(parent), R, W_in, W_out, st))
+        size = s.element_size()
+        rows, stride, row_bytes = _row_layout(s.shape, s.stride(), size)
+        if o is s:
+            o_rows, o_stride, o_bytes = rows, stride, row_bytes
+        else:
+            o_rows, o_stride, o_bytes = _row_layout(o.shape, o.stride(), size)
+            if o.dtype != s.dtype or o.shape[1:] != s.shape[1:]:
+                raise ValueError(f"state {i}: its out differs in row shape or type")
+        if rows != R * W_in or o_rows != R * W_out:
+            raise ValueError(f"state {i}: expected rows [R*W_in, ...] and an out [R*W_out, ...]")
+        flat += (o.data_ptr(), s.data_ptr(), o_stride, stride, row_bytes)
+    call, par = L.load().tr_beam_reorder, _ptr(parent)
+    for i in range(0, len(states), L.TR_MAX_STATES):
+        m = min(L.TR_MAX_STATES, len(states) - i)
+        packed = struct.pack("=" + "QQqqq" * m, *flat[5 * i:5 * (i + m)])
+        _run(dev, stream, call, C.cast(packed, C.POINTER(L.BeamState)), m, par, R, W_in, W_out)
     return dsts
 
 
