@@ -1,10 +1,13 @@
-// Attention of sequences that share their request's prefix (tr_prefix_attention).
+// Attention of sequences that share their request's prefix (tr_prefix_attention): the plan, and the
+// kernels that add each sequence's own keys and merge.
 //
 // For query token (s, t) and head h of request r, over the request's prefix keys and then the
 // keys of the sequence's own suffix:
 //     a_j = scale q.k_j,   m = max_j a_j,   l = sum_j exp(a_j - m),   o = sum_j exp(a_j - m) v_j / l
 // with m, l and o carried from key to key (a new maximum rescales l and o), so that no score is
-// ever stored.  Exponentials are powers of two: a_j is kept times log2(e).
+// ever stored.  Exponentials are powers of two: a_j is kept times log2(e).  The prefix part runs
+// once per request for all of its sequences (prefix_attention_tc.cu, prefix_attention_f32.cu) and
+// leaves one or, of a split prefix, several normalised partial results per row.
 #include <math.h>
 
 #include <algorithm>
@@ -15,8 +18,6 @@ namespace tr {
 namespace attn {
 namespace {
 
-constexpr int kRowWarps = 4;
-
 __device__ __forceinline__ int request_of(const AttnParams& p, int64_t s) {
   int lo = 0, hi = p.R - 1;        // the last request that starts at or before s and is not empty
   while (lo < hi) {
@@ -24,79 +25,6 @@ __device__ __forceinline__ int request_of(const AttnParams& p, int64_t s) {
     if (p.req[mid].s0 <= s) lo = mid; else hi = mid - 1;
   }
   return lo;
-}
-
-// One warp per (s, t, head): 32 keys at a time, each lane one key's product with the query, then
-// each lane some of the output columns.
-template <typename T>
-__global__ void __launch_bounds__(kRowWarps * 32) attn_row_kernel(const __grid_constant__ AttnParams p) {
-  __shared__ float sq[kRowWarps][kMaxDHead];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t row = (int64_t)blockIdx.x * kRowWarps + warp;
-  if (row >= p.n_rows) return;
-  const int D = p.d.d_head, H = p.d.n_head;
-  const int h = (int)(row % H);
-  const int64_t st = row / H, s = st / p.d.L_t;
-  const int t = (int)(st % p.d.L_t), hk = h / (H / p.d.n_kv_head);
-  const int r = request_of(p, s);
-  const T* q = static_cast<const T*>(p.q) + st * p.d.q_token + (int64_t)h * D;
-  for (int i = lane; i < D; i += 32) sq[warp][i] = to_f32(q[i]);
-  __syncwarp();
-  const float c = p.d.scale * kLog2e;
-  float m = -INFINITY, l = 0.f, o[kMaxDHead / 32] = {};
-  auto keys = [&](const T* k, const T* v, int64_t stride, int64_t n) {
-    for (int64_t j0 = 0; j0 < n; j0 += 32) {
-      const int64_t j = j0 + lane;
-      float a = -INFINITY;
-      if (j < n) {
-        const T* kr = k + j * stride;
-        constexpr int N = 16 / sizeof(T);
-        float acc = 0.f;
-        for (int i = 0; i < D; i += N) {
-          T kv[N];
-          *reinterpret_cast<uint4*>(kv) = *reinterpret_cast<const uint4*>(kr + i);
-#pragma unroll
-          for (int e = 0; e < N; ++e) acc = fmaf(sq[warp][i + e], to_f32(kv[e]), acc);
-        }
-        a = acc * c;
-      }
-      float bm = a;
-#pragma unroll
-      for (int x = 16; x; x >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
-      const float nm = fmaxf(m, bm);
-      const float base = nm == -INFINITY ? 0.f : nm;    // keys of -inf weigh nothing, NaN stays NaN
-      const float f = exp2f(m - base), w = exp2f(a - base);
-      float ws = w;
-#pragma unroll
-      for (int x = 16; x; x >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, x);
-      l = l * f + ws;
-      m = nm;
-#pragma unroll
-      for (int i = 0; i < kMaxDHead / 32; ++i) o[i] *= f;
-      const int cnt = (int)min((int64_t)32, n - j0);
-      for (int e = 0; e < cnt; ++e) {
-        const float we = __shfl_sync(0xffffffffu, w, e);
-        const T* vr = v + (j0 + e) * stride;
-#pragma unroll
-        for (int i = 0; i < kMaxDHead / 32; ++i)
-          if (lane + 32 * i < D) o[i] = fmaf(we, to_f32(vr[lane + 32 * i]), o[i]);
-      }
-    }
-  };
-  const RequestPlan& rq = p.req[r];
-  {
-    const int64_t po = rq.p0 * p.d.prefix_token + hk * p.d.prefix_head;
-    keys(static_cast<const T*>(p.k_prefix) + po, static_cast<const T*>(p.v_prefix) + po, p.d.prefix_token, rq.p1 - rq.p0);
-  }
-  const int64_t so = s * p.d.suffix_seq + hk * p.d.suffix_head;
-  keys(static_cast<const T*>(p.k_suffix) + so, static_cast<const T*>(p.v_suffix) + so, p.d.suffix_token,
-       visible_suffix(p, s, t));
-  T* out = static_cast<T*>(p.out) + row * D;
-  const float inv = l == 0.f ? 0.f : 1.f / l;   // (a NaN score gives a NaN row)
-#pragma unroll
-  for (int i = 0; i < kMaxDHead / 32; ++i)
-    if (lane + 32 * i < D) out[lane + 32 * i] = from_f32<T>(o[i] * inv);
-  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // The suffix part of every row, and the merge with the prefix part's partial results.  A team of
@@ -497,11 +425,11 @@ tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t
   return TR_OK;
 }
 
-// How many steps of 128 keys a unit takes.  Fewer steps give more units to spread over the SMs,
-// but every unit costs about three tile steps (Q, the first scores, the result) and every chunk of
-// a prefix a partial result per row.  The candidates are: no split, and the shortest chunks that
-// give one, two or four units per SM.
-void plan_units(AttnParams& p, int sms) {
+// How many steps of keys a unit takes.  Fewer steps give more units to spread over the `slots` (SMs,
+// or CTAs that share one), but every unit costs about three tile steps (Q, the first scores, the
+// result) and every chunk of a prefix a partial result per row.  The candidates are: no split, and
+// the shortest chunks that give one, two or four units per slot.
+void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots) {
   const int G = p.d.n_head / p.d.n_kv_head;
   int steps[TR_MAX_REQUESTS], n_m[TR_MAX_REQUESTS];
   int longest = 0;
@@ -509,9 +437,9 @@ void plan_units(AttnParams& p, int sms) {
   bool two = false;
   for (int r = 0; r < p.R; ++r) {
     const int64_t m = (int64_t)(p.req[r].s1 - p.req[r].s0) * p.d.L_t * G;
-    steps[r] = m > 0 ? ceil_div(p.req[r].p1 - p.req[r].p0, kStepKeys) : 0;
-    n_m[r] = ceil_div(m, kUnitRows);
-    two = two || m > kUnitRows / 2;
+    steps[r] = m > 0 ? ceil_div(p.req[r].p1 - p.req[r].p0, step_keys) : 0;
+    n_m[r] = ceil_div(m, unit_rows);
+    two = two || m > unit_rows / 2;
     longest = std::max(longest, steps[r]);
     rows_all += request_rows(p, r);
   }
@@ -528,12 +456,12 @@ void plan_units(AttnParams& p, int sms) {
       int lo = 1, hi = longest;               // units(c) falls with c
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
-        if (units(mid) <= (int64_t)w * sms) hi = mid; else lo = mid + 1;
+        if (units(mid) <= (int64_t)w * slots) hi = mid; else lo = mid + 1;
       }
       c = lo;
     }
     // tile steps of the busiest SM (about 0.7 us each), and the partial results' traffic
-    const double waves = (double)((units(c) + sms - 1) / sms);
+    const double waves = (double)((units(c) + slots - 1) / slots);
     const double split = (double)ceil_div(longest, c);
     const double bytes = split > 1 ? (double)rows_all * split * p.d.d_head * 8.0 : 0.0;
     const double cost = waves * (c * (two ? 2.0 : 1.0) + 3.0) + bytes / 3.5e6;
@@ -557,11 +485,10 @@ void plan_units(AttnParams& p, int sms) {
   p.req[p.R].part = part;
 }
 
-// The plan of a call; p.n_units is 0 where the row kernel reads the prefixes itself.
 struct Plan {
   bool direct = false;        // the tensor-core kernel writes the results
   size_t bytes = 0;
-  int sms = 0;
+  int sms = 0, unit_rows = 0;
 };
 tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* prefix, int R, AttnParams& p, Plan& plan) {
   TR_TRY(check_offsets(d, seq, prefix, R));
@@ -575,10 +502,19 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
     q.s1 = (int)seq[std::min(r + 1, R)];
     q.p1 = (int)prefix[std::min(r + 1, R)];
   }
-  p.n_units = 0;
   TR_TRY(sm_count(&plan.sms));
-  if (d->dtype != TR_BF16) return TR_OK;
-  plan_units(p, plan.sms);
+  if (d->dtype == TR_F32) {
+    // two CTAs per SM; units of 16 rows waste less of the few rows of small batches, units of 64
+    // read K and V a quarter as often
+    int64_t most = 0;
+    for (int r = 0; r < R; ++r) most = std::max(most, (seq[r + 1] - seq[r]) * d->L_t * (d->n_head / d->n_kv_head));
+    plan.unit_rows = most <= 32 ? 16 : 64;
+    plan_units(p, plan.unit_rows, kStepKeysF32, 2 * plan.sms);
+    plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);
+    return TR_OK;
+  }
+  plan.unit_rows = kUnitRows;
+  plan_units(p, kUnitRows, kStepKeys, plan.sms);
   plan.direct = d->suffix_cap <= kDirectSuffix;
   for (int r = 0; r < R; ++r) plan.direct = plan.direct && (p.req[r].n_split == 1 || p.req[r].s0 == p.req[r].s1);
   if (!plan.direct) plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);
@@ -634,14 +570,12 @@ extern "C" tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q
   p.status = ds->status;
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + p.req[R].part * desc->d_head;
+  if (desc->dtype == TR_F32) {
+    if (p.n_units > 0) TR_TRY(launch_prefix_f32(p, plan.unit_rows, st));
+    return launch_finish<float>(p, plan.sms, st);
+  }
   if (p.n_units > 0) TR_TRY(launch_prefix_tc(p, plan.direct, st));
   if (plan.direct) return TR_OK;
-  if (desc->dtype == TR_BF16) {
-    if (desc->suffix_cap >= 8) return desc->d_head <= 64 ? launch_suffix<1>(p, st) : launch_suffix<2>(p, st);
-    return launch_finish<__nv_bfloat16>(p, plan.sms, st);
-  }
-  const unsigned grid = (unsigned)((p.n_rows + kRowWarps - 1) / kRowWarps);
-  attn_row_kernel<float><<<grid, kRowWarps * 32, 0, st>>>(p);
-  TR_LAUNCH_CHECK("attn_row_kernel");
-  return TR_OK;
+  if (desc->suffix_cap >= 8) return desc->d_head <= 64 ? launch_suffix<1>(p, st) : launch_suffix<2>(p, st);
+  return launch_finish<__nv_bfloat16>(p, plan.sms, st);
 }

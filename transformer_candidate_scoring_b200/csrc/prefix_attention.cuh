@@ -10,11 +10,13 @@ namespace attn {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxDHead = 128;
-constexpr int kStepKeys = 128;      // keys of one step of the tensor-core kernel
-constexpr int kUnitRows = 256;      // query rows of a unit (two tiles of 128)
+// Query rows of a unit and keys of a step: of the tensor-core kernel (two tiles of 128 rows), and
+// of the fp32 one, whose units are 64 rows, or 16 where no key head has more than 32.
+constexpr int kUnitRows = 256, kStepKeys = 128;
+constexpr int kStepKeysF32 = 64;
 
 // The prefix part of one request: rows = sequences x query tokens x heads of a key head.  A unit
-// is up to 256 rows of one key head over `chunk` steps of 128 keys; a prefix of several chunks
+// is up to `unit_rows` of them of one key head over `chunk` steps of keys; a prefix of several chunks
 // gives each row several partial results.
 struct RequestPlan {
   int first_unit;      // units of request r: first_unit[r] .. first_unit[r+1]-1
@@ -44,6 +46,40 @@ __host__ __device__ inline int64_t request_rows(const AttnParams& p, int r) {
   return (int64_t)(p.req[r].s1 - p.req[r].s0) * p.d.L_t * p.d.n_head;
 }
 
+struct Unit {
+  int r, hk, m0, rows, split;
+  int tok, keys;       // first key token, keys of this chunk
+  int steps;
+  bool two;            // tensor-core kernel: the two tiles hold different rows
+  __device__ int jobs(int t) const { return two ? steps : (steps + 1 - t) / 2; }
+  __device__ int step_of(int t, int k) const { return two ? k : 2 * k + t; }   // step of tile t's k-th job
+};
+
+__device__ __forceinline__ Unit unit_at(const AttnParams& p, int u, int unit_rows, int step_keys) {
+  int lo = 0, hi = p.R - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.req[mid].first_unit <= u) lo = mid; else hi = mid - 1;
+  }
+  const RequestPlan& q = p.req[lo];
+  const int m_all = (q.s1 - q.s0) * p.d.L_t * (p.d.n_head / p.d.n_kv_head);
+  const int n_m = (m_all + unit_rows - 1) / unit_rows;
+  int i = u - q.first_unit;
+  Unit x;
+  x.r = lo;
+  x.m0 = (i % n_m) * unit_rows;      // units that share keys are neighbours
+  i /= n_m;
+  x.split = i % q.n_split;
+  x.hk = i / q.n_split;
+  x.rows = min(unit_rows, m_all - x.m0);
+  x.two = x.rows > unit_rows / 2;
+  const int k0 = x.split * q.chunk * step_keys;
+  x.tok = q.p0 + k0;
+  x.keys = min(q.chunk * step_keys, q.p1 - x.tok);
+  x.steps = (x.keys + step_keys - 1) / step_keys;
+  return x;
+}
+
 // Suffix keys that query token t of sequence s sees; a length outside the buffer is clamped.
 __device__ __forceinline__ int visible_suffix(const AttnParams& p, int64_t s, int t) {
   if (p.d.suffix_cap == 0) return 0;
@@ -60,6 +96,8 @@ __device__ __forceinline__ int visible_suffix(const AttnParams& p, int64_t s, in
 // the row's own keys and writes out and lse instead.
 constexpr int kDirectSuffix = 4;
 tr_status launch_prefix_tc(const AttnParams& p, bool direct, cudaStream_t st);
+// The fp32 kernel over every unit (of 64 or 16 rows).
+tr_status launch_prefix_f32(const AttnParams& p, int unit_rows, cudaStream_t st);
 
 }  // namespace attn
 }  // namespace tr

@@ -113,40 +113,6 @@ struct Bars {
   uint32_t ml_full, ml_empty;
 };
 
-struct Unit {
-  int r, hk, m0, rows, split;
-  int tok, keys;       // first key token, keys of this chunk
-  int steps;
-  bool two;            // the two tiles hold different rows
-  __device__ int jobs(int t) const { return two ? steps : (steps + 1 - t) / 2; }
-  __device__ int step_of(int t, int k) const { return two ? k : 2 * k + t; }   // step of tile t's k-th job
-};
-
-__device__ __forceinline__ Unit unit_at(const AttnParams& p, int u) {
-  int lo = 0, hi = p.R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.req[mid].first_unit <= u) lo = mid; else hi = mid - 1;
-  }
-  const RequestPlan& q = p.req[lo];
-  const int m_all = (q.s1 - q.s0) * p.d.L_t * (p.d.n_head / p.d.n_kv_head);
-  const int n_m = (m_all + kUnitRows - 1) / kUnitRows;
-  int i = u - q.first_unit;
-  Unit x;
-  x.r = lo;
-  x.m0 = (i % n_m) * kUnitRows;      // units that share keys are neighbours
-  i /= n_m;
-  x.split = i % q.n_split;
-  x.hk = i / q.n_split;
-  x.rows = min(kUnitRows, m_all - x.m0);
-  x.two = x.rows > kM;
-  const int k0 = x.split * q.chunk * kN;
-  x.tok = q.p0 + k0;
-  x.keys = min(q.chunk * kN, q.p1 - x.tok);
-  x.steps = (x.keys + kN - 1) / kN;
-  return x;
-}
-
 // One thread: streams the K (or V) steps of every unit into its ring.
 template <int DH>
 __device__ void load_steps(const AttnParams& p, const CUtensorMap* map, uint32_t ring, int slots, uint32_t full, uint32_t empty,
@@ -156,7 +122,7 @@ __device__ void load_steps(const AttnParams& p, const CUtensorMap* map, uint32_t
   bool ok = true;
   uint32_t pending = 0, par = 0;           // bit s: a load of slot s was issued, and its parity
   for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-    const Unit x = unit_at(p, u);
+    const Unit x = unit_at(p, u, kUnitRows, kN);
     for (int j = 0; j < x.steps; ++j) {
       if (!(ok = mbar_wait_idle(empty + 8 * s, ph ^ 1, abort_flag))) break;
       const uint32_t dst = ring + s * Smem<DH>::TILE;
@@ -185,7 +151,7 @@ __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, cons
   uint32_t kph = 0, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
   bool ok = true;
   for (int u = blockIdx.x; u < p.a.n_units && ok; u += gridDim.x) {
-    const Unit x = unit_at(p.a, u);
+    const Unit x = unit_at(p.a, u, kUnitRows, kN);
     const int n_jobs = x.two ? 2 * x.steps : x.steps;
     auto qk = [&](int i) {
       const int t = i & 1, step = x.two ? i >> 1 : i;
@@ -260,7 +226,7 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
   uint32_t sph = 0, oph = 0, xph = 0;
   bool ok = true;
   for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-    const Unit x = unit_at(p, u);
+    const Unit x = unit_at(p, u, kUnitRows, kN);
     const RequestPlan& rq = p.req[x.r];
     const int base = x.two ? t * kM : 0;
     const bool live = base + tid < x.rows, warp_live = base + wrow < x.rows;
