@@ -18,6 +18,12 @@
 //   warps 0-3, 4-7      softmax of tile 0 and 1, one row per thread, and the epilogue
 //   warps 8, 9, 10      K loads, V loads, MMA issue; warp 11 owns the tensor memory
 //
+// A step's chain -- S, softmax, P V, of which the next S waits because P lies where S was -- bounds
+// many rows: about 3,600 cycles for both tiles' 128 keys, of which the tensor core is busy 2,048
+// (855 TFLOP/s over 8,192 sequences, 16 heads of 128 on 4 key heads and 4,096 keys).  Steps of 64 keys with two S buffers
+// per tile, separate S and P with steps of 80 keys, one MMA warp per tile, two threads per row and a part
+// of the exponentials on the FMA pipes measured no faster (319 to 427 us against 322).
+//
 // The row maximum that O and l are relative to is raised only when the new one is more than 2^8
 // away (then O is rescaled in TMEM): numerators stay below 2^8 and sums in fp32 range.  Values
 // behind a prefix are kept out twice: their scores are replaced by -inf, and the V rows that the
@@ -98,7 +104,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // A warp's wait; every lane gives up when one does.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+// One lane of a converged warp.  The compiler knows this instruction to pick a single lane and keeps the
+// operands of the MMAs under it in uniform registers; under `lane == 0` it does not, and each issue
+// took 80 to 120 cycles instead of the product's own 64.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // acc + the products of two bf16 pairs.
@@ -107,9 +122,14 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
   return fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u), acc);
 }
 
+// The 16-byte piece c of row r of a Q tile.
+__device__ __forceinline__ uint32_t piece(uint32_t tile, int r, int c) {
+  return tile + r * 128 + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4);
+}
+
 struct Bars {
   uint32_t kfull, kempty, vfull, vempty;   // rings, 8 bytes apart
-  uint32_t qfull, sfull, pfull, odone;     // per tile
+  uint32_t qfull, sfull, pfull, odone;     // per tile (pfull: two per tile)
   uint32_t ml_full, ml_empty;
 };
 
@@ -141,77 +161,131 @@ __device__ void load_steps(const AttnParams& p, const CUtensorMap* map, uint32_t
   }
 }
 
-// The whole warp: lane 0 issues, all lanes zero V rows behind the prefix.
+// The whole warp: one lane issues, all lanes zero V rows behind the prefix.
 template <int DH>
 __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, const Bars& b, int lane, volatile int* abort_flag) {
   using L = Smem<DH>;
   const int dk = (p.a.d.d_head + 15) / 16;                 // 16-wide slices of d_head
-  const uint32_t id_o = idesc_bf16(kM, dk * 16) | kBMajorMN;
+  const uint32_t id_o = idesc_bf16(kM, dk * 16) | kBMajorMN, id_full = idesc_bf16(kM, kN);
+  const uint64_t q0 = desc_k(smem + L::Q), k0 = desc_k(smem + L::K), v0 = desc_mn(smem + L::V, 128 * 128);
   int ks = 0, vs = 0;                                      // ring slots of the current step
   uint32_t kph = 0, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
   bool ok = true;
   for (int u = blockIdx.x; u < p.a.n_units && ok; u += gridDim.x) {
     const Unit x = unit_at(p.a, u, kUnitRows, kN);
-    const int n_jobs = x.two ? 2 * x.steps : x.steps;
+    const bool two = x.two;
+    const int n_jobs = two ? 2 * x.steps : x.steps;
+    const int last = x.keys - (x.steps - 1) * kN;          // keys of the last step
     auto qk = [&](int i) {
-      const int t = i & 1, step = x.two ? i >> 1 : i;
+      const int t = i & 1, step = two ? i >> 1 : i;
       if (i < 2) {
         ok = ok && wait_all(b.qfull + 8 * t, qph[t], abort_flag);
         qph[t] ^= 1;
       }
       ok = ok && wait_all(b.kfull + 8 * ks, kph, abort_flag);
       if (!ok) return;
-      const int n = (min(kN, x.keys - step * kN) + 15) & ~15;
+      const bool done = !two || t == 1;                    // nothing reads these keys any more
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t qa = smem + L::Q + t * L::TILE, ka = smem + L::K + ks * L::TILE, id = idesc_bf16(kM, n);
-        for (int kk = 0; kk < dk; ++kk) {
-          const uint32_t o = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-          mma_bf16(tmem + t * kN, desc_k(qa + o), desc_k(ka + o), id, kk > 0);
-        }
+      if (elect_one()) {
+        const uint64_t qa = q0 + t * (L::TILE >> 4), ka = k0 + ks * (L::TILE >> 4);
+        const uint32_t id = step == x.steps - 1 ? idesc_bf16(kM, (last + 15) & ~15) : id_full;
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk)
+          if (kk < dk) {
+            const uint64_t o = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+            mma_bf16(tmem + t * kN, qa + o, ka + o, id, kk > 0);
+          }
         mma_commit(b.sfull + 8 * t);
-        if (!x.two || t == 1) mma_commit(b.kempty + 8 * ks);
+        if (done) mma_commit(b.kempty + 8 * ks);
       }
-      if (!x.two || t == 1)
-        if (++ks == L::NK) { ks = 0; kph ^= 1; }
+      if (done && ++ks == L::NK) { ks = 0; kph ^= 1; }
     };
     qk(0);
     if (n_jobs > 1) qk(1);
     for (int i = 0; i < n_jobs && ok; ++i) {
-      const int t = i & 1, k = i >> 1, step = x.two ? k : i;
-      const int valid = min(kN, x.keys - step * kN);
-      ok = wait_all(b.vfull + 8 * vs, vph, abort_flag);
-      const uint32_t va = smem + L::V + vs * L::TILE;
-      if (ok && (valid & 15) && (t == 0 || !x.two)) {
-        // rows valid .. the end of their 16-key slice: 16-byte pieces of the 128-byte rows
-        const int n_rows = 16 - (valid & 15);
-        for (int c = lane; c < n_rows * 8 * (DH / 64); c += 32) {
-          const int h = c / (n_rows * 8), rr = (c / 8) % n_rows;
-          st_shared_v4(va + h * (128 * 128) + (valid + rr) * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
+      const int t = i & 1, k = i >> 1, step = two ? k : i;
+      const int valid = step == x.steps - 1 ? last : kN;
+      const bool done = !two || t == 1;
+      if (t == 0 || !two) {
+        ok = wait_all(b.vfull + 8 * vs, vph, abort_flag);
+        if (ok && (valid & 15)) {
+          // rows valid .. the end of their 16-key slice: 16-byte pieces of the 128-byte rows
+          const uint32_t va = smem + L::V + vs * L::TILE;
+          const int n_rows = 16 - (valid & 15);
+          for (int c = lane; c < n_rows * 8 * (DH / 64); c += 32) {
+            const int h = c / (n_rows * 8), rr = (c / 8) % n_rows;
+            st_shared_v4(va + h * (128 * 128) + (valid + rr) * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        fence_proxy_async_smem();
-        __syncwarp();
       }
-      ok = ok && wait_all(b.pfull + 8 * t, pph[t], abort_flag);
+      const uint64_t va = v0 + vs * (L::TILE >> 4);
+      const int nk = (valid + 15) / 16;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {               // P comes in two halves of 64 keys
+        ok = ok && wait_all(b.pfull + 8 * (2 * t + half), pph[t], abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = half * (kN / 32); kk < (half + 1) * (kN / 32); ++kk)
+            if (kk < nk)
+              mma_bf16_ta(tmem + 2 * kN + t * 128, tmem + t * kN + kk * 8, va + kk * (2048 >> 4), id_o, (k > 0 || kk > 0) ? 1u : 0u);
+          if (half == 1) {
+            if (done) mma_commit(b.vempty + 8 * vs);
+            if (i + 2 >= n_jobs) mma_commit(b.odone + 8 * t);
+          }
+        }
+      }
       pph[t] ^= 1;
       if (!ok) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const int nk = (valid + 15) / 16;
-        for (int kk = 0; kk < nk; ++kk)
-          mma_bf16_ta(tmem + 2 * kN + t * 128, tmem + t * kN + kk * 8, desc_mn(va + kk * 2048, 128 * 128), id_o,
-                      (k > 0 || kk > 0) ? 1u : 0u);
-        if (!x.two || t == 1) mma_commit(b.vempty + 8 * vs);
-        if (i + 2 >= n_jobs) mma_commit(b.odone + 8 * t);
-      }
-      if (!x.two || t == 1)
-        if (++vs == L::NV) { vs = 0; vph ^= 1; }
+      if (done && ++vs == L::NV) { vs = 0; vph ^= 1; }
       if (i + 2 < n_jobs) qk(i + 2);
     }
   }
 }
 
-// A softmax warpgroup (tile t): loads its Q rows, turns S into P step by step, writes the result.
+// What a softmax thread knows of its row of a unit.
+struct Row {
+  Unit x;
+  int base, jobs;        // the tile's first row in the unit, its steps
+  bool live, warp_live;
+  int64_t token;         // query token of the batch
+  int head;
+};
+__device__ __forceinline__ Row row_at(const AttnParams& p, int u, int t, int tid) {
+  Row r;
+  r.x = unit_at(p, u, kUnitRows, kN);
+  r.base = r.x.two ? t * kM : 0;
+  r.jobs = r.x.jobs(t);
+  r.live = r.base + tid < r.x.rows;
+  r.warp_live = r.base + (tid & ~31) < r.x.rows;
+  const int G = p.d.n_head / p.d.n_kv_head, m = r.x.m0 + r.base + tid;     // row within (request, key head)
+  r.token = (int64_t)p.req[r.x.r].s0 * p.d.L_t + m / G;
+  r.head = r.x.hk * G + m % G;
+  return r;
+}
+// This thread's row of Q into the Q tile, eight 16-byte pieces in flight.
+template <int DH>
+__device__ __forceinline__ void fill_q(const AttnParams& p, const Row& r, uint32_t tile, int tid) {
+  const int D = p.d.d_head;
+  const bool in = r.live && r.jobs > 0;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                  (in ? r.token * p.d.q_token + (int64_t)r.head * D : 0));
+#pragma unroll
+  for (int i0 = 0; i0 < DH / 8; i0 += 8) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = in && (i0 + i) * 8 < D ? __ldg(q + i0 + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i0 + i) * 8 < D + 8) st_shared_v4(piece(tile, tid, i0 + i), v[i].x, v[i].y, v[i].z, v[i].w);
+  }
+}
+
+// A softmax warpgroup (tile t): turns S into P step by step and writes the result.  The Q rows of its next
+// unit are on their way while this one's result is written.
 template <int DH>
 __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t smem, float* sml, const Bars& b,
                              volatile int* abort_flag) {
@@ -219,31 +293,22 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
   const AttnParams& p = tp.a;
   const int tid = threadIdx.x & 127, lane = tid & 31, wrow = tid & ~31;    // wrow: the warp's first row
   const uint32_t lanes = (uint32_t)wrow << 16;                              // its TMEM lanes
+  const uint32_t q_tile = smem + L::Q + t * L::TILE;
   const uint32_t s_addr = tmem + t * kN + lanes, o_addr = tmem + 2 * kN + t * 128 + lanes;
-  const int D = p.d.d_head, G = p.d.n_head / p.d.n_kv_head;
+  const int D = p.d.d_head;
   const float c = p.d.scale * kLog2e;
   const uint64_t c2 = f32x2(c, c);
   uint32_t sph = 0, oph = 0, xph = 0;
   bool ok = true;
+  Row next = row_at(p, blockIdx.x, t, tid);
+  fill_q<DH>(p, next, q_tile, tid);
   for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-    const Unit x = unit_at(p, u, kUnitRows, kN);
+    const Row rw = next;
+    const Unit& x = rw.x;
     const RequestPlan& rq = p.req[x.r];
-    const int base = x.two ? t * kM : 0;
-    const bool live = base + tid < x.rows, warp_live = base + wrow < x.rows;
-    const int m = x.m0 + base + tid;                         // row within (request, key head)
-    const int64_t token = (int64_t)rq.s0 * p.d.L_t + m / G;  // query token of the batch
-    const int head = x.hk * G + m % G;
-    const int jobs = x.jobs(t);
+    const bool live = rw.live, warp_live = rw.warp_live;
+    const int jobs = rw.jobs;
     if (jobs > 0) {
-      // ---- Q rows (the previous unit's products have read them: its last S was seen)
-      const uint32_t row = smem + L::Q + t * L::TILE + tid * 128;
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + token * p.d.q_token + (int64_t)head * D);
-      const int chunks = D / 8, pad = ((D + 15) / 16) * 2;
-#pragma unroll 4
-      for (int i = 0; i < pad; ++i) {
-        const uint4 v = live && i < chunks ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
-        st_shared_v4(row + (i >> 3) * (128 * 128) + (((i & 7) ^ (tid & 7)) << 4), v.x, v.y, v.z, v.w);
-      }
       fence_proxy_async_smem();
       mbar_arrive(b.qfull + 8 * t);
     }
@@ -254,8 +319,9 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
       if (!(ok = wait_all(b.sfull + 8 * t, sph, abort_flag))) break;
       sph ^= 1;
       tc_fence_after();
+      float mc = 0.f;
+      float s[kN];
       if (warp_live) {
-        float s[kN];
 #pragma unroll
         for (int i = 0; i < kN / 32; ++i)
           if (i * 32 < valid) tmem_ld32(s_addr + 32 * i, s + 32 * i);
@@ -296,165 +362,181 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
             tmem_wait_st();
           }
         }
-        const float mc = mx == -INFINITY ? 0.f : mx * c;      // keys of -inf weigh nothing, NaN stays NaN
-        const uint64_t mc2 = f32x2(-mc, -mc);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < kN / 32; ++i)
-          if (i * 32 < valid) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float a, bb;
-              f32x2_split(fma_f32x2(f32x2(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), c2, mc2), a, bb);
-              a = ex2(a);
-              bb = ex2(bb);
-              sum[e & 1] = add_f32x2(sum[e & 1], f32x2(a, bb));
-              w[e] = pack_bf16(a, bb);
-            }
-            asm volatile(
-                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-                    s_addr + 16 * i),
-                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
-                "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
-                : "memory");
-          }
-        float a0, a1;
-        f32x2_split(add_f32x2(sum[0], sum[1]), a0, a1);
-        l += a0 + a1;
-        tmem_wait_st();
-        tc_fence_before();
+        mc = mx == -INFINITY ? 0.f : mx * c;              // keys of -inf weigh nothing, NaN stays NaN
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b.pfull + 8 * t);
+      const uint64_t mc2 = f32x2(-mc, -mc);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (warp_live) {
+#pragma unroll
+          for (int i = 2 * half; i < 2 * half + 2; ++i)
+            if (i * 32 < valid) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float a, bb;
+                f32x2_split(fma_f32x2(f32x2(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), c2, mc2), a, bb);
+                a = ex2(a);
+                bb = ex2(bb);
+                sum[e & 1] = add_f32x2(sum[e & 1], f32x2(a, bb));
+                w[e] = pack_bf16(a, bb);
+              }
+              asm volatile(
+                  "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                      s_addr + 16 * i),
+                  "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
+                  "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+                  : "memory");
+            }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.pfull + 8 * (2 * t + half));
+      }
+      float a0, a1;
+      f32x2_split(add_f32x2(sum[0], sum[1]), a0, a1);
+      l += a0 + a1;
     }
     if (!ok) break;
+    // ---- with `direct`, the row's own few keys: their scores, from the Q row in shared memory
+    const int64_t seq = rw.token / p.d.L_t;
+    const int64_t own = seq * p.d.suffix_seq + (int64_t)x.hk * p.d.suffix_head;
+    float a[kDirectSuffix];
+    int n_own = 0, n_warp = 0;
+    const bool writes = warp_live && (x.two || t == 0);
+    if (writes && tp.direct && p.d.suffix_cap > 0) {
+      n_own = live ? visible_suffix(p, seq, (int)(rw.token - seq * p.d.L_t)) : 0;
+      n_warp = __reduce_max_sync(0xffffffffu, n_own);
+#pragma unroll
+      for (int j = 0; j < kDirectSuffix; ++j) {
+        a[j] = -INFINITY;
+        if (j < n_own) {
+          const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_suffix) + own + j * p.d.suffix_token);
+          float acc = 0.f;
+#pragma unroll 2
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 kv = __ldg(kr + i);
+            uint4 qv;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(qv.x), "=r"(qv.y), "=r"(qv.z), "=r"(qv.w)
+                         : "r"(piece(q_tile, tid, i)));
+            acc = dot2(qv.x, kv.x, dot2(qv.y, kv.y, dot2(qv.z, kv.z, dot2(qv.w, kv.w, acc))));
+          }
+          a[j] = acc * c;
+        }
+      }
+    }
+    // ---- the next unit's Q sets out
+    const bool more = u + gridDim.x < p.n_units;
+    if (more) next = row_at(p, u + gridDim.x, t, tid);
     // ---- the result of the unit's rows
     if (jobs > 0) {
       if (!(ok = wait_all(b.odone + 8 * t, oph, abort_flag))) break;
       oph ^= 1;
     }
-    float w0 = 1.f, w1 = 0.f, lsum = l, mref = mx;
-    if (!x.two) {
+    if (!x.two && t == 1) {
       // both tiles hold these rows: tile 1 hands its maximum and sum over, tile 0 reads its O
-      if (t == 1) {
-        sml[tid] = jobs > 0 ? mx : -INFINITY;
-        sml[128 + tid] = l;
-        tc_fence_before();
-        mbar_arrive(b.ml_full);
-        ok = wait_all(b.ml_empty, xph, abort_flag);
-        xph ^= 1;
-        continue;
-      }
-      if (!(ok = wait_all(b.ml_full, xph, abort_flag))) break;
+      sml[tid] = jobs > 0 ? mx : -INFINITY;
+      sml[128 + tid] = l;
+      tc_fence_before();
+      mbar_arrive(b.ml_full);
+      ok = wait_all(b.ml_empty, xph, abort_flag);
       xph ^= 1;
-      const float m1 = sml[tid], l1 = sml[128 + tid];
-      mref = fmaxf(mx, m1);
-      const float mb = mref == -INFINITY ? 0.f : mref;
-      w0 = mx == mref ? 1.f : ex2((mx - mb) * c);
-      w1 = m1 == mref ? 1.f : ex2((m1 - mb) * c);
-      lsum = w0 * l + w1 * l1;
-    }
-    tc_fence_after();
-    const bool second = !x.two && x.steps > 1;               // tile 1 has an O
-    if (warp_live) {
-      const int64_t row = token * p.d.n_head + head;
-      // ---- with `direct`, the row's own few keys join here: their scores from the Q row in shared
-      // memory, their values beside O below
-      const int64_t seq = token / p.d.L_t;
-      const int64_t own = seq * p.d.suffix_seq + (int64_t)x.hk * p.d.suffix_head;
-      float a[kDirectSuffix], ref = __fmul_rn(mref, c);
-      int n_own = 0, n_warp = 0;
-      if (tp.direct && p.d.suffix_cap > 0) {
-        n_own = live ? visible_suffix(p, seq, (int)(token % p.d.L_t)) : 0;
-        n_warp = __reduce_max_sync(0xffffffffu, n_own);
-        float top = ref;
-#pragma unroll
-        for (int j = 0; j < kDirectSuffix; ++j) {
-          a[j] = -INFINITY;
-          if (j < n_own) {
-            const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_suffix) + own + j * p.d.suffix_token);
-            const uint32_t qr = smem + L::Q + t * L::TILE + tid * 128;
-            float acc = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-              const uint4 kv = __ldg(kr + i);
-              uint4 qv;
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(qv.x), "=r"(qv.y), "=r"(qv.z), "=r"(qv.w)
-                           : "r"(qr + (i >> 3) * (128 * 128) + (((i & 7) ^ (tid & 7)) << 4)));
-              acc = dot2(qv.x, kv.x, dot2(qv.y, kv.y, dot2(qv.z, kv.z, dot2(qv.w, kv.w, acc))));
-            }
-            a[j] = acc * c;
-            top = fmaxf(top, a[j]);
-          }
-        }
-        const float tb = top == -INFINITY ? 0.f : top, f = ref == top ? 1.f : ex2(ref - tb);
-        lsum *= f;
-        w0 *= f;
-        w1 *= f;
-#pragma unroll
-        for (int j = 0; j < kDirectSuffix; ++j) {
-          a[j] = ex2(a[j] - tb);
-          lsum += a[j];
-        }
-        ref = top;
+    } else {
+      float w0 = 1.f, w1 = 0.f, lsum = l, mref = mx;
+      if (!x.two) {
+        if (!(ok = wait_all(b.ml_full, xph, abort_flag))) break;
+        xph ^= 1;
+        const float m1 = sml[tid], l1 = sml[128 + tid];
+        mref = fmaxf(mx, m1);
+        const float mb = mref == -INFINITY ? 0.f : mref;
+        w0 = mx == mref ? 1.f : ex2((mx - mb) * c);
+        w1 = m1 == mref ? 1.f : ex2((m1 - mb) * c);
+        lsum = w0 * l + w1 * l1;
       }
-      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-      const float lse2 = lsum == 0.f ? -INFINITY : ref + log2f(lsum);
-      const int64_t part = rq.part + x.split * request_rows(p, x.r) + (row - (int64_t)rq.s0 * p.d.L_t * p.d.n_head);
-      for (int i = 0; i * 16 < D; ++i) {
-        float o[16], o1[16];
-        tmem_ld16(o_addr + 16 * i, o);
-        if (second) tmem_ld16(o_addr + 128 + 16 * i, o1);
-        tmem_wait_ld();
-        reg_fence<16>(o);
-        reg_fence<16>(o1);
+      tc_fence_after();
+      const bool second = !x.two && x.steps > 1;             // tile 1 has an O
+      if (warp_live) {
+        const int64_t row = rw.token * p.d.n_head + rw.head;
+        float ref = __fmul_rn(mref, c);
+        if (n_warp > 0) {
+          float top = ref;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = second ? o[e] * w0 + o1[e] * w1 : o[e] * w0;
+          for (int j = 0; j < kDirectSuffix; ++j) top = fmaxf(top, a[j]);
+          const float tb = top == -INFINITY ? 0.f : top, f = ref == top ? 1.f : ex2(ref - tb);
+          lsum *= f;
+          w0 *= f;
+          w1 *= f;
 #pragma unroll
-        for (int j = 0; j < kDirectSuffix; ++j)
-          if (j < n_warp) {
-            const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_suffix) + own + j * p.d.suffix_token) + 2 * i;
+          for (int j = 0; j < kDirectSuffix; ++j) {
+            a[j] = ex2(a[j] - tb);
+            lsum += a[j];
+          }
+          ref = top;
+        }
+        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+        const float lse2 = lsum == 0.f ? -INFINITY : ref + log2f(lsum);
+        const int64_t part = rq.part + x.split * request_rows(p, x.r) + (row - (int64_t)rq.s0 * p.d.L_t * p.d.n_head);
+        w0 *= inv;
+        w1 *= inv;
+#pragma unroll
+        for (int j = 0; j < kDirectSuffix; ++j) a[j] *= inv;
+#pragma unroll 2
+        for (int i = 0; i < (D + 15) / 16; ++i) {
+          float o[16], o1[16];
+          tmem_ld16(o_addr + 16 * i, o);
+          if (second) tmem_ld16(o_addr + 128 + 16 * i, o1);
+          tmem_wait_ld();
+          reg_fence<16>(o);
+          reg_fence<16>(o1);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = second ? o[e] * w0 + o1[e] * w1 : o[e] * w0;
+          if (n_warp > 0) {
+#pragma unroll
+            for (int j = 0; j < kDirectSuffix; ++j) {
+              const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_suffix) + own + j * p.d.suffix_token) + 2 * i;
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (j < n_own && 16 * i + 8 * h < D) {
+                  const uint4 v = __ldg(vr + h);
+                  const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    o[8 * h + 2 * e] = fmaf(a[j], __uint_as_float(vw[e] << 16), o[8 * h + 2 * e]);
+                    o[8 * h + 2 * e + 1] = fmaf(a[j], __uint_as_float(vw[e] & 0xFFFF0000u), o[8 * h + 2 * e + 1]);
+                  }
+                }
+            }
+          }
+          if (live) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              if (j < n_own && 16 * i + 8 * h < D) {
-                const uint4 v = __ldg(vr + h);
-                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  o[8 * h + 2 * e] = fmaf(a[j], __uint_as_float(vw[e] << 16), o[8 * h + 2 * e]);
-                  o[8 * h + 2 * e + 1] = fmaf(a[j], __uint_as_float(vw[e] & 0xFFFF0000u), o[8 * h + 2 * e + 1]);
+              if (16 * i + 8 * h < D) {
+                if (tp.direct) {
+                  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D + 16 * i + 8 * h) =
+                      make_uint4(pack_bf16(o[8 * h], o[8 * h + 1]), pack_bf16(o[8 * h + 2], o[8 * h + 3]),
+                                 pack_bf16(o[8 * h + 4], o[8 * h + 5]), pack_bf16(o[8 * h + 6], o[8 * h + 7]));
+                } else {
+                  float4* d = reinterpret_cast<float4*>(p.part_o + part * D + 16 * i + 8 * h);
+                  d[0] = make_float4(o[8 * h], o[8 * h + 1], o[8 * h + 2], o[8 * h + 3]);
+                  d[1] = make_float4(o[8 * h + 4], o[8 * h + 5], o[8 * h + 6], o[8 * h + 7]);
                 }
               }
           }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] *= inv;
+        }
         if (live) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (16 * i + 8 * h < D) {
-              if (tp.direct) {
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D + 16 * i + 8 * h) =
-                    make_uint4(pack_bf16(o[8 * h], o[8 * h + 1]), pack_bf16(o[8 * h + 2], o[8 * h + 3]),
-                               pack_bf16(o[8 * h + 4], o[8 * h + 5]), pack_bf16(o[8 * h + 6], o[8 * h + 7]));
-              } else {
-                float4* d = reinterpret_cast<float4*>(p.part_o + part * D + 16 * i + 8 * h);
-                d[0] = make_float4(o[8 * h], o[8 * h + 1], o[8 * h + 2], o[8 * h + 3]);
-                d[1] = make_float4(o[8 * h + 4], o[8 * h + 5], o[8 * h + 6], o[8 * h + 7]);
-              }
-            }
+          if (!tp.direct)
+            p.part_lse[part] = lse2;
+          else if (p.lse)
+            p.lse[row] = lse2 * kLn2;
         }
       }
-      if (live) {
-        if (!tp.direct)
-          p.part_lse[part] = lse2;
-        else if (p.lse)
-          p.lse[row] = lse2 * kLn2;
-      }
+      tc_fence_before();
+      if (!x.two) mbar_arrive(b.ml_empty);
     }
-    tc_fence_before();
-    if (!x.two) mbar_arrive(b.ml_empty);
+    if (more) fill_q<DH>(p, next, q_tile, tid);
   }
 }
 
@@ -469,11 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   uint32_t at = smem + L::BAR;
   auto take = [&](int n) { const uint32_t r = at; at += 8 * n; return r; };
   b.kfull = take(L::NK); b.kempty = take(L::NK); b.vfull = take(L::NV); b.vempty = take(L::NV);
-  b.qfull = take(2); b.sfull = take(2); b.pfull = take(2); b.odone = take(2);
+  b.qfull = take(2); b.sfull = take(2); b.pfull = take(4); b.odone = take(2);
   b.ml_full = take(1); b.ml_empty = take(1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::BAR + 248);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::BAR + 252);
-  static_assert((2 * L::NK + 2 * L::NV + 10) * 8 <= 248, "barriers");
+  static_assert((2 * L::NK + 2 * L::NV + 12) * 8 <= 248, "barriers");
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < L::NK; ++i) { mbar_init(b.kfull + 8 * i, 1); mbar_init(b.kempty + 8 * i, 1); }
@@ -481,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     for (int t = 0; t < 2; ++t) {
       mbar_init(b.qfull + 8 * t, 128);
       mbar_init(b.sfull + 8 * t, 1);
-      mbar_init(b.pfull + 8 * t, 4);
+      mbar_init(b.pfull + 16 * t, 4);
+      mbar_init(b.pfull + 16 * t + 8, 4);
       mbar_init(b.odone + 8 * t, 1);
     }
     mbar_init(b.ml_full, 128);
