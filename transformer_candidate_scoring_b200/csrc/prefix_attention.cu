@@ -226,138 +226,128 @@ tr_status launch_finish(const AttnParams& p, int sms, cudaStream_t st) {
                    : launch_finish<T, 16>(p, sms, st);
 }
 
-// The same for bf16 suffixes of eight tokens and more, on warp-level matrix instructions: the L_t x
-// (n_head / n_kv_head) rows of a sequence that share a key head are one 16-row operand against
-// 16 of its keys at a time, so each key and value is read once for all of them, straight into the
-// fragments of the products (the order of d_head within a product is free, so a lane's 16 bytes
-// of a key are its share of two slices; of values, of eight column tiles).  `parts` warps share a
-// sequence's keys; all meet in shared memory, where the prefix part's results join.
+// The same for bf16 suffixes of eight tokens and more, on warp-level matrix instructions: of the L_t x
+// (n_head / n_kv_head) rows of a sequence that share a key head, eight are the columns of
+// S^T = K Q^T (16 keys x 8 rows) and of O^T += V^T P^T, so each key and value is read once for all of them,
+// straight into the fragments of the products (the order of d_head within a product is free, so a
+// lane's 16 bytes of a key are its share of two slices, and of values its share of eight).  P^T
+// turns from a result into an operand by a transpose between lanes.  `parts` warps share a
+// sequence's keys; all meet in shared memory, where the prefix part's results join.  The read of the
+// keys and values bounds it: a warp has 16 of each in flight.
 constexpr int kSuffixThreads = 128;
 
-__device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values, lane l holding columns 2 (l % 4), + 1 of row l / 4, to its transpose.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
 }
 
 template <int kBlocks>     // 64-wide blocks of d_head
-__global__ void __launch_bounds__(kSuffixThreads) suffix_kernel(const __grid_constant__ AttnParams p, int parts, int m_tiles) {
+__global__ void __launch_bounds__(kSuffixThreads, kBlocks == 1 ? 6 : 4)
+suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
   constexpr int DP = kBlocks * 64;
-  __shared__ float s_o[kSuffixThreads / 32][16][DP + 4], s_m[kSuffixThreads / 32][16], s_l[kSuffixThreads / 32][16];
+  __shared__ float s_o[kSuffixThreads / 32][8][DP + 4], s_m[kSuffixThreads / 32][8], s_l[kSuffixThreads / 32][8];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4;
   const int units = kSuffixThreads / 32 / parts, part = warp % parts, D = p.d.d_head, H = p.d.n_head, Hk = p.d.n_kv_head;
   const int G = H / Hk, n_rows = p.d.L_t * G;
-  const int64_t n_unit = (int64_t)p.req[p.R].s0 * Hk * m_tiles;
-  const int64_t u_at = (int64_t)blockIdx.x * units + warp / parts, u = min(u_at, n_unit - 1);
-  const int mt = (int)(u % m_tiles), hk = (int)(u / m_tiles % Hk);
-  const int64_t s = u / m_tiles / Hk;
-  const int row0 = mt * 16;                               // of the sequence's rows of this key head: t * G + head in group
+  const int n_unit = p.req[p.R].s0 * Hk * r_tiles;         // below 2^31: no more than query rows
+  const int u_at = blockIdx.x * units + warp / parts, u = min(u_at, n_unit - 1);
+  const int s = u / (Hk * r_tiles), hk = u / r_tiles % Hk, row0 = u % r_tiles * 8;   // rows t * G + head in group
   const float c = p.d.scale * kLog2e;
-  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q);
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  // ---- Q: 16 bytes of rows g and g + 8 per 32 columns
-  uint4 q[2][2 * kBlocks];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = row0 + g + 8 * h;
-    const __nv_bfloat16* src = qp + (s * p.d.L_t + r / G) * p.d.q_token + (int64_t)(hk * G + r % G) * D;
+  const int len = visible_suffix(p, s, p.d.L_t - 1);       // what the last query token sees: all of it
+  // ---- Q: 16 bytes of row g per 32 columns
+  uint4 q[2 * kBlocks];
+  {
+    const int r = row0 + g;
+    const __nv_bfloat16* src =
+        static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)s * p.d.L_t + r / G) * p.d.q_token + (hk * G + r % G) * D;
 #pragma unroll
     for (int i = 0; i < 2 * kBlocks; ++i)
-      q[h][i] = r < n_rows && i * 32 + qd * 8 < D ? __ldg(reinterpret_cast<const uint4*>(src + i * 32 + qd * 8)) : zero;
+      q[i] = r < n_rows && i * 32 + qd * 8 < D ? __ldg(reinterpret_cast<const uint4*>(src + i * 32 + qd * 8)) : zero;
   }
-  // keys seen by rows g, g + 8 and, at most, by any row of the sequence
-  const int t0 = min((row0 + g) / G, p.d.L_t - 1), t1 = min((row0 + g + 8) / G, p.d.L_t - 1);
-  const int n0 = visible_suffix(p, s, t0), n1 = visible_suffix(p, s, t1), n = visible_suffix(p, s, p.d.L_t - 1);
-  const int64_t so = s * p.d.suffix_seq + hk * p.d.suffix_head;
+  // keys that rows 2 qd and 2 qd + 1 see
+  int seen[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    seen[e] = p.d.causal ? max(0, len - max(0, p.d.L_t - 1 - (row0 + 2 * qd + e) / G)) : len;
+  const int64_t so = (int64_t)s * p.d.suffix_seq + hk * p.d.suffix_head;
   const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(p.k_suffix) + so, *vp = static_cast<const __nv_bfloat16*>(p.v_suffix) + so;
-  float o[8 * kBlocks][4] = {};
+  float o[4 * kBlocks][4] = {};                            // O^T: 16 columns of d_head x 8 rows
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  for (int j0 = part * 16; j0 < n; j0 += parts * 16) {
+  for (int j0 = part * 16; j0 < len; j0 += parts * 16) {
     uint4 k[2][2 * kBlocks], v[4][kBlocks];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int j = j0 + g + 8 * h;
+      const __nv_bfloat16* src = kp + j * p.d.suffix_token + qd * 8;
 #pragma unroll
       for (int i = 0; i < 2 * kBlocks; ++i)
-        k[h][i] = j < n && i * 32 + qd * 8 < D ? __ldg(reinterpret_cast<const uint4*>(kp + j * p.d.suffix_token + i * 32 + qd * 8)) : zero;
+        k[h][i] = j < len && i * 32 + qd * 8 < D ? __ldg(reinterpret_cast<const uint4*>(src + i * 32)) : zero;
     }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       const int j = j0 + 2 * qd + (h & 1) + (h >> 1) * 8;
+      const __nv_bfloat16* src = vp + j * p.d.suffix_token + g * 8;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
-        v[h][b] = j < n && b * 64 + g * 8 < D ? __ldg(reinterpret_cast<const uint4*>(vp + j * p.d.suffix_token + b * 64 + g * 8)) : zero;
+        v[h][b] = j < len && b * 64 + g * 8 < D ? __ldg(reinterpret_cast<const uint4*>(src + b * 64)) : zero;
     }
-    float sc[2][4] = {};
+    float st[4] = {};                                      // keys g (0, 1) and g + 8 (2, 3) x rows 2 qd, 2 qd + 1
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 2 * kBlocks; ++i) {
-        const uint32_t a0[4] = {q[0][i].x, q[1][i].x, q[0][i].y, q[1][i].y}, a1[4] = {q[0][i].z, q[1][i].z, q[0][i].w, q[1][i].w};
-        mma_16816(sc[h], a0, k[h][i].x, k[h][i].y);
-        mma_16816(sc[h], a1, k[h][i].z, k[h][i].w);
-      }
-    // rows g (r = 0) and g + 8 (r = 1); columns 2 qd, 2 qd + 1 of each key tile h
-    uint32_t w[2][2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int seen = r ? n1 : n0;
-      float a[4], top = m[r];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + (e >> 1) * 8 + 2 * qd + (e & 1);
-        a[e] = j < seen ? sc[e >> 1][2 * r + (e & 1)] * c : -INFINITY;
-        top = fmaxf(top, a[e]);
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float base = top == -INFINITY ? 0.f : top, f = exp2f(m[r] - base);
-      m[r] = top;
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        a[e] = exp2f(a[e] - base);
-        sum += a[e];
-      }
-      l[r] = l[r] * f + sum;
-      w[r][0] = bf16x2(a[0], a[1]);
-      w[r][1] = bf16x2(a[2], a[3]);
-#pragma unroll
-      for (int i = 0; i < 8 * kBlocks; ++i) {
-        o[i][2 * r] *= f;
-        o[i][2 * r + 1] *= f;
-      }
+    for (int i = 0; i < 2 * kBlocks; ++i) {
+      mma_16816(st, k[0][i].x, k[1][i].x, k[0][i].y, k[1][i].y, q[i].x, q[i].y);
+      mma_16816(st, k[0][i].z, k[1][i].z, k[0][i].w, k[1][i].w, q[i].z, q[i].w);
     }
-    const uint32_t a[4] = {w[0][0], w[1][0], w[0][1], w[1][1]};
+    float f[2];
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
+    for (int e = 0; e < 2; ++e) {
+      const float a0 = j0 + g < seen[e] ? st[e] * c : -INFINITY, a1 = j0 + g + 8 < seen[e] ? st[2 + e] * c : -INFINITY;
+      float top = fmaxf(m[e], fmaxf(a0, a1));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t x[4];
+      for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float base = top == -INFINITY ? 0.f : top;     // keys of -inf weigh nothing, NaN stays NaN
+      f[e] = exp2f(m[e] - base);
+      m[e] = top;
+      st[e] = exp2f(a0 - base);
+      st[2 + e] = exp2f(a1 - base);
+      l[e] = l[e] * f[e] + st[e] + st[2 + e];              // (this lane's keys only)
+    }
+    const uint32_t b0 = transpose_8x8(bf16x2(st[0], st[1])), b1 = transpose_8x8(bf16x2(st[2], st[3]));
 #pragma unroll
-        for (int h = 0; h < 4; ++h) x[h] = (&v[h][b].x)[i / 2];
-        const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
-        mma_16816(o[b * 8 + i], a, __byte_perm(x[0], x[1], sel), __byte_perm(x[2], x[3], sel));
-      }
+    for (int i = 0; i < 4 * kBlocks; ++i) {
+      // rows of A: columns 8 g' + 2 i' and + 1 of the block, g' = 0 .. 7 in lanes' order
+      const int b = i / 4, w = i % 4;
+      uint32_t x[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) x[h] = (&v[h][b].x)[w];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] *= f[e & 1];
+      mma_16816(o[i], __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x5410),
+                __byte_perm(x[2], x[3], 0x7632), b0, b1);
+    }
   }
-  // ---- rows g, g + 8: columns b * 64 + 16 qd + i (and + 8 + i) of column tile (b, i)
+  // ---- o[i][0], [1]: column b * 64 + 8 g + 2 w of rows 2 qd, 2 qd + 1; [2], [3]: the next column
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    if (qd == 0) {
-      s_m[warp][g + 8 * r] = m[r];
-      s_l[warp][g + 8 * r] = l[r];
+  for (int e = 0; e < 2; ++e) {
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+    if (g == 0) {
+      s_m[warp][2 * qd + e] = m[e];
+      s_l[warp][2 * qd + e] = l[e];
     }
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        float* d = &s_o[warp][g + 8 * r][b * 64 + 16 * qd + i];
-        *reinterpret_cast<float4*>(d) = make_float4(o[b * 8 + i][2 * r], o[b * 8 + i + 1][2 * r], o[b * 8 + i + 2][2 * r], o[b * 8 + i + 3][2 * r]);
-        *reinterpret_cast<float4*>(d + 8) = make_float4(o[b * 8 + i][2 * r + 1], o[b * 8 + i + 1][2 * r + 1], o[b * 8 + i + 2][2 * r + 1],
-                                                        o[b * 8 + i + 3][2 * r + 1]);
-      }
+    for (int b = 0; b < kBlocks; ++b) {
+      float* d = &s_o[warp][2 * qd + e][b * 64 + 8 * g];
+      *reinterpret_cast<float4*>(d) = make_float4(o[4 * b][e], o[4 * b][2 + e], o[4 * b + 1][e], o[4 * b + 1][2 + e]);
+      *reinterpret_cast<float4*>(d + 4) = make_float4(o[4 * b + 2][e], o[4 * b + 2][2 + e], o[4 * b + 3][e], o[4 * b + 3][2 + e]);
+    }
   }
   cudaGridDependencySynchronize();
   __syncthreads();
@@ -366,9 +356,9 @@ __global__ void __launch_bounds__(kSuffixThreads) suffix_kernel(const __grid_con
   const RequestPlan& rq = p.req[request_of(p, s)];
   const int64_t rows = (int64_t)(rq.s1 - rq.s0) * p.d.L_t * H;
   const int chunks = D / 8, first = warp / parts * parts;
-  for (int item = part * 32 + lane; item < min(16, n_rows - row0) * chunks; item += parts * 32) {
+  for (int item = part * 32 + lane; item < min(8, n_rows - row0) * chunks; item += parts * 32) {
     const int rr = item / chunks, c0 = item % chunks * 8, r = row0 + rr;
-    const int64_t row = (s * p.d.L_t + r / G) * H + hk * G + r % G;
+    const int64_t row = ((int64_t)s * p.d.L_t + r / G) * H + hk * G + r % G;
     Running x;
     for (int i = 0; i < parts; ++i) {
       const float mm = s_m[first + i][rr];
@@ -376,8 +366,10 @@ __global__ void __launch_bounds__(kSuffixThreads) suffix_kernel(const __grid_con
       x.rescale(fmaxf(x.m, mm), &base);
       const float f = exp2f(mm - base);
       x.l = fmaf(f, s_l[first + i][rr], x.l);
+      const float4 y = *reinterpret_cast<const float4*>(&s_o[first + i][rr][c0]), z = *reinterpret_cast<const float4*>(&s_o[first + i][rr][c0 + 4]);
+      const float w[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x.o[e] = fmaf(f, s_o[first + i][rr][c0 + e], x.o[e]);
+      for (int e = 0; e < 8; ++e) x.o[e] = fmaf(f, w[e], x.o[e]);
     }
     merge_prefix(p, rq, rq.part + (row - (int64_t)rq.s0 * p.d.L_t * H), rows, c0, true, 0, 1, x);
     store_row<__nv_bfloat16>(p, row, c0, x);
@@ -389,10 +381,10 @@ template <int kBlocks>
 tr_status launch_suffix(const AttnParams& p, cudaStream_t st) {
   // a warp per 16 keys up to the four of a CTA
   const int steps = (p.d.suffix_cap + 15) / 16, parts = steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
-  const int m_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 15) / 16, units = kSuffixThreads / 32 / parts;
-  const int64_t n_unit = (int64_t)p.req[p.R].s0 * p.d.n_kv_head * m_tiles;
+  const int r_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 7) / 8, units = kSuffixThreads / 32 / parts;
+  const int64_t n_unit = (int64_t)p.req[p.R].s0 * p.d.n_kv_head * r_tiles;
   return launch_dependent(suffix_kernel<kBlocks>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
-                          parts, m_tiles);
+                          parts, r_tiles);
 }
 
 tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t* prefix, int R) {
