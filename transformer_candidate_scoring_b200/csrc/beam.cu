@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kSumThreads = 256;
 constexpr int kVecs = 8;                 // 16-byte vectors per lane
-constexpr int kPickThreads = 512;
+constexpr int kPickThreads = 1024;
 constexpr int kPickTiles = 1024, kPickGroups = 1023;   // tiles and groups noted for a closer look
 constexpr int kPickCap = 1536;           // candidates the final sort takes
 constexpr int kTokenBits = 24;
@@ -284,10 +284,11 @@ __device__ __forceinline__ unsigned long long tie_of(int beam, float x, int toke
 }
 
 // One warp, n keys per lane: a key, at least `floor`, that at least `want` of them reach (that many
-// are known to reach `floor`), and not many more than that.  A step tries three keys, whose counts (at
-// most 512 each) share one reduction.
+// are known to reach `floor`), and not many more than that.  A step tries two keys, whose counts
+// share one reduction.
 template <int n, typename F>
 __device__ __forceinline__ uint32_t bisect(F load, int want, uint32_t floor) {
+  static_assert(n * 32 < 1 << 16, "counts");
   uint32_t key[n], a = ~0u, b = 0;
 #pragma unroll
   for (int i = 0; i < n; ++i) {
@@ -298,19 +299,15 @@ __device__ __forceinline__ uint32_t bisect(F load, int want, uint32_t floor) {
   a = __reduce_min_sync(0xffffffffu, a);
   b = max(a, __reduce_max_sync(0xffffffffu, b));
   while (a < b) {
-    const uint32_t q = (b - a + 3) / 4, m1 = min(a + q, b), m2 = min(m1 + q, b), m3 = min(m2 + q, b);
+    const uint32_t q = (b - a + 2) / 3, m1 = min(a + q, b), m2 = min(m1 + q, b);
     uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < n; ++i) c += (key[i] >= m1 ? 1u : 0u) + (key[i] >= m2 ? 1u << 10 : 0u) + (key[i] >= m3 ? 1u << 20 : 0u);
+    for (int i = 0; i < n; ++i) c += (key[i] >= m1 ? 1u : 0u) + (key[i] >= m2 ? 1u << 16 : 0u);
     c = __reduce_add_sync(0xffffffffu, c);
-    const int c1 = c & 1023, c2 = c >> 10 & 1023, c3 = c >> 20;
+    const int c1 = c & 0xFFFF, c2 = c >> 16;
     int got = 0;
-    if (c3 >= want) {
-      a = m3;
-      got = c3;
-    } else if (c2 >= want) {
+    if (c2 >= want) {
       a = m2;
-      b = m3 - 1;
       got = c2;
     } else if (c1 >= want) {
       a = m1;
