@@ -286,13 +286,13 @@ __device__ __forceinline__ unsigned long long tie_of(int beam, float x, int toke
 // One warp, n keys per lane: a key, at least `floor`, that at least `want` of them reach (that many
 // are known to reach `floor`), and not many more than that.  A step tries two keys, whose counts
 // share one reduction.
-template <int n, typename F>
-__device__ __forceinline__ uint32_t bisect(F load, int want, uint32_t floor) {
+template <int n>
+__device__ __forceinline__ uint32_t bisect_by(const uint32_t* keys, int want, uint32_t floor) {
   static_assert(n * 32 < 1 << 16, "counts");
   uint32_t key[n], a = ~0u, b = 0;
 #pragma unroll
   for (int i = 0; i < n; ++i) {
-    key[i] = load(i);
+    key[i] = keys[i * 32 + (threadIdx.x & 31)];
     a = min(a, max(key[i], floor));
     b = max(b, key[i]);
   }
@@ -320,6 +320,10 @@ __device__ __forceinline__ uint32_t bisect(F load, int want, uint32_t floor) {
   }
   return a;
 }
+// Over the first `count` of at most 1024 keys (those behind them, up to the next power of two, are 0).
+__device__ __forceinline__ uint32_t bisect(const uint32_t* keys, int count, int want, uint32_t floor) {
+  return count <= 128 ? bisect_by<4>(keys, want, floor) : count <= 512 ? bisect_by<16>(keys, want, floor) : bisect_by<32>(keys, want, floor);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ SelectParams p) {
@@ -340,17 +344,17 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   cudaGridDependencySynchronize();
   // ---- a warp per beam: the row's maximum and sum, then a thread per beam: its log-sum-exp
   for (int b = warp; b < p.W; b += kWarps) {
+    constexpr int kHeld = 4;                            // tiles per lane held between the two steps
+    float4 y[kHeld];                                    // (unwritten where the row offers nothing)
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      y[i] = lane + 32 * i < p.n_tile ? __ldcg(reinterpret_cast<const float4*>(sums + b * p.n_tile + lane + 32 * i))
+                                      : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
     const float cum = p.cum[row0 + b];
     int kind = isfinite(cum) ? p.finished && p.finished[row0 + b] ? 2 : 1 : 0;
     float M = -INFINITY;
     double S = 0.0;
     if (kind == 1) {
-      constexpr int kHeld = 4;                          // tiles per lane held between the two steps
-      float4 y[kHeld];
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        y[i] = lane + 32 * i < p.n_tile ? __ldcg(reinterpret_cast<const float4*>(sums + b * p.n_tile + lane + 32 * i))
-                                        : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) M = fmaxf(M, y[i].x);
       for (int c = lane + 32 * kHeld; c < p.n_tile; c += 32) M = fmaxf(M, __ldcg(&sums[b * p.n_tile + c].max));
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   // fewer than k threads have one.
   uint32_t lo = kKeyNegInf + 1;
   float upper;
-  auto bound_of = [&](auto&& each) {
+  auto bound_of = [&](auto&& each, int keys) {         // keys: threads that may have one, from the first on
     float mine = -INFINITY;
     upper = -INFINITY;
     each([&](int, int, float t, float e) {
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     s_key[tid] = okey(mine);
     if (__syncthreads_count(mine > -INFINITY) < k) return false;
     if (warp == 0) {
-      const uint32_t cut = bisect<kPickThreads / 32>([&](int i) { return s_key[i * 32 + lane]; }, k, lo);
+      const uint32_t cut = bisect(s_key, keys, k, lo);
       if (lane == 0) s_cut = cut;
     }
     __syncthreads();
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       }
     }
   };
-  bool by_tile = bound_of(each_tile);
+  bool by_tile = bound_of(each_tile, n_tile);
   if (by_tile) {
     bound = of_key(lo);
     if (upper >= bound)
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   __syncthreads();
   if (s_groups > kPickGroups) {
     // too many to note: a bound from the groups themselves, and once more
-    bound_of(each_group);
+    bound_of(each_group, kPickThreads);
     bound = of_key(lo);
     if (tid == 0) s_groups = 0;
     __syncthreads();
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     for (int i = n + tid; i < kPickGroups + 1; i += kPickThreads) s_key[i] = 0u;
     __syncthreads();
     if (warp == 0) {
-      const uint32_t cut = bisect<(kPickGroups + 1) / 32>([&](int i) { return s_key[i * 32 + lane]; }, k, lo);
+      const uint32_t cut = bisect(s_key, n, k, lo);
       if (lane == 0) s_cut = cut;
     }
     __syncthreads();
@@ -527,7 +531,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     bound = of_key(lo);
   }
   const int n_scan = (noted ? s_groups : n_group) * kVecs;
-  // f(rank) for every token of those groups that may reach the bound: a vector at a time
+  // f(beam, logit, token) for every token of those groups that may reach the bound, a vector at a time; a
+  // finished beam gives its pad token
   auto each = [&](auto f) {
     for (int j = tid; j < n_scan; j += kPickThreads) {
       int b, i;
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
         i = j / kVecs % per_row;
       }
       const int kind = s_kind[b];
-      if (kind == 2 && i == 0 && j % kVecs == 0) f(Rank{okey(s_cum[b]), tie_of(b, 0.f, p.pad_token)});
+      if (kind == 2 && i == 0 && j % kVecs == 0) f(b, 0.f, p.pad_token);
       if (kind != 1) continue;
       const int v = (i / 32) * tile_elems<T>() + (j % kVecs) * 32 * N + (i % 32) * N;
       if (v >= p.V) continue;
@@ -553,25 +558,31 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
         const float x = P::at(w[e / (N / 4)], e);
         if (x > -INFINITY && (bits >> e & 1u)) {
           const Near y = near_of(b, x);
-          if (y.t + y.e >= bound) {
-            const unsigned long long key = key_of(b, x);
-            if (key) f(Rank{key, tie_of(b, x, v + e)});
-          }
+          if (y.t + y.e >= bound) f(b, x, v + e);
         }
       }
     }
   };
-  each([&](const Rank& q) {
+  auto rank_of = [&](int b, float x, int token) {
+    return Rank{s_kind[b] == 2 ? okey(s_cum[b]) : key_of(b, x), tie_of(b, x, token)};
+  };
+  each([&](int b, float x, int token) {
     const int at = atomicAdd(&s_count, 1);
-    if (at < kPickCap) s_rank[at] = q;
+    if (at < kPickCap) s_rank[at] = Rank{(unsigned long long)__float_as_uint(x), tie_of(b, x, token)};
   });
   __syncthreads();
   int count = s_count;
-  if (count > kPickCap) {
+  if (count <= kPickCap) {
+    for (int i = tid; i < count; i += kPickThreads) {      // (their exact totals, now that each has a thread)
+      const int b = 255 - (int)(s_rank[i].tie >> 56);
+      s_rank[i].key = s_kind[b] == 2 ? okey(s_cum[b]) : key_of(b, __uint_as_float((uint32_t)s_rank[i].key));
+    }
+    __syncthreads();
+  } else {
     // too many: the exact k-th candidate, by its total and then by its tie
     auto count_if = [&](auto pred) {
       int c = 0;
-      each([&](const Rank& q) { c += pred(q); });
+      each([&](int b, float x, int token) { c += pred(rank_of(b, x, token)); });
       __syncthreads();
       if (tid == 0) s_count = 0;
       __syncthreads();
@@ -593,7 +604,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     __syncthreads();
     if (tid == 0) s_count = 0;
     __syncthreads();
-    each([&](const Rank& q) {
+    each([&](int b, float x, int token) {
+      const Rank q = rank_of(b, x, token);
       if (q.key > a || (q.key == a && q.tie >= ta)) s_rank[atomicAdd(&s_count, 1)] = q;   // exactly k (ties differ)
     });
     __syncthreads();
@@ -601,13 +613,13 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   }
   // the totals rounded to fp32 order the candidates but for ties; those that may be among the k best
   uint32_t cut = 0u, mykey = 0u;
-  for (int i = tid; i < count; i += kPickThreads) mykey = max(mykey, s_key[i] = okey((float)of_key(s_rank[i].key)));
+  for (int i = tid; i < count; i += kPickThreads) mykey = max(mykey, s_key[i] = s_rank[i].key ? okey((float)of_key(s_rank[i].key)) : 0u);
   if (tid == 0) s_groups = 0;
   if (count > 2 * k + 32) {
     s_best[tid] = mykey;
     if (__syncthreads_count(mykey > 0u) >= k) {
       if (warp == 0) {
-        const uint32_t c = bisect<kPickThreads / 32>([&](int i) { return s_best[i * 32 + lane]; }, k, 1u);
+        const uint32_t c = bisect(s_best, count, k, 1u);
         if (lane == 0) s_cut = c;
       }
       __syncthreads();
@@ -627,9 +639,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   __syncthreads();
   auto put = [&](int j, const Rank& q) {
     const int64_t at = (int64_t)r * k + j;
-    p.parent[at] = 255 - (int)(q.tie >> 56);
-    p.token[at] = (1 << kTokenBits) - 1 - (int)(q.tie & ((1u << kTokenBits) - 1));
-    p.score[at] = (float)of_key(q.key);
+    const bool some = q.key != 0ull;                       // (0: a total of -inf)
+    p.parent[at] = some ? 255 - (int)(q.tie >> 56) : -1;
+    p.token[at] = some ? (1 << kTokenBits) - 1 - (int)(q.tie & ((1u << kTokenBits) - 1)) : -1;
+    p.score[at] = some ? (float)of_key(q.key) : -INFINITY;
   };
   // each of them counts those before it
   const uint4* key4 = reinterpret_cast<const uint4*>(s_sel_key);
