@@ -121,6 +121,11 @@ ATTN = [
     ([2], [5000], 4, 4, 32, 130, 1, False),                  # a long prefix for few rows
     ([300, 2], [1100, 700], 8, 4, 64, 2, 1, False),
     ([1], [2], 64, 1, 128, 300, 1, False),
+    ([3, 2, 4], [0, 50, 0], 4, 2, 64, 1, 1, False),          # one own key, requests without a prefix
+    ([3, 2, 140], [0, 50, 0], 4, 2, 128, 0, 1, False),
+    ([5, 66], [0, 3], 8, 2, 32, 1, 2, True),
+    ([150, 9], [260, 0], 4, 1, 96, 1, 1, False),
+    ([130, 7], [300, 0], 2, 1, 104, 4, 4, True),
 ]
 
 

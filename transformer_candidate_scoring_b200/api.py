@@ -382,10 +382,10 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
         lse = _new(q.shape[:-1], torch.float32, dev, stream)
     elif lse.shape != q.shape[:-1] or lse.dtype != torch.float32:
         raise ValueError("lse: expected fp32 of q's shape without the last dimension")
-    ws, size = _workspace(workspace, need, dev, stream)
+    ws, size = _workspace(workspace, need, dev, stream) if need else (None, 0)
     _run(dev, stream, L.load().tr_prefix_attention, desc, q.data_ptr(), so, k_prefix.data_ptr(), v_prefix.data_ptr(), po,
          k_suffix.data_ptr() if S else None, v_suffix.data_ptr() if S else None, suffix_len.data_ptr() if S else None, R,
-         _ptr(out), _ptr(lse), ws.data_ptr(), size)
+         _ptr(out), _ptr(lse), ws.data_ptr() if need else None, size)
     return out, lse
 
 

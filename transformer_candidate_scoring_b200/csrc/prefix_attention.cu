@@ -420,8 +420,9 @@ tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t
 // How many steps of keys a unit takes.  Fewer steps give more units to spread over the `slots` (SMs,
 // or CTAs that share one), but every unit costs about three tile steps (Q, the first scores, the
 // result) and every chunk of a prefix a partial result per row.  The candidates are: no split, and
-// the shortest chunks that give one, two or four units per slot.
-void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots) {
+// the shortest chunks that give one, two or four units per slot.  With `direct`, no split also saves the
+// merge's launch (about 4 us), and requests without a prefix have one (empty) unit per 256 rows.
+void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool direct) {
   const int G = p.d.n_head / p.d.n_kv_head;
   int steps[TR_MAX_REQUESTS], n_m[TR_MAX_REQUESTS];
   int longest = 0;
@@ -456,7 +457,7 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots) {
     const double waves = (double)((units(c) + slots - 1) / slots);
     const double split = (double)ceil_div(longest, c);
     const double bytes = split > 1 ? (double)rows_all * split * p.d.d_head * 8.0 : 0.0;
-    const double cost = waves * (c * (two ? 2.0 : 1.0) + 3.0) + bytes / 3.5e6;
+    const double cost = waves * (c * (two ? 2.0 : 1.0) + 3.0) + bytes / 3.5e6 + (direct && split > 1 ? 6.0 : 0.0);
     if (cost < best_cost) {
       best_cost = cost;
       best = c;
@@ -469,6 +470,7 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots) {
     q.first_unit = unit;
     q.chunk = best;
     q.n_split = ceil_div(steps[r], best);
+    if (direct && best >= longest && q.s1 > q.s0) q.n_split = 1;
     q.part = part;
     unit += p.d.n_kv_head * n_m[r] * q.n_split;
     part += request_rows(p, r) * q.n_split;
@@ -501,12 +503,12 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
     int64_t most = 0;
     for (int r = 0; r < R; ++r) most = std::max(most, (seq[r + 1] - seq[r]) * d->L_t * (d->n_head / d->n_kv_head));
     plan.unit_rows = most <= 32 ? 16 : 64;
-    plan_units(p, plan.unit_rows, kStepKeysF32, 2 * plan.sms);
+    plan_units(p, plan.unit_rows, kStepKeysF32, 2 * plan.sms, false);
     plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);
     return TR_OK;
   }
   plan.unit_rows = kUnitRows;
-  plan_units(p, kUnitRows, kStepKeys, plan.sms);
+  plan_units(p, kUnitRows, kStepKeys, plan.sms, d->suffix_cap <= kDirectSuffix);
   plan.direct = d->suffix_cap <= kDirectSuffix;
   for (int r = 0; r < R; ++r) plan.direct = plan.direct && (p.req[r].n_split == 1 || p.req[r].s0 == p.req[r].s1);
   if (!plan.direct) plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);

@@ -92,9 +92,9 @@ __device__ __forceinline__ int visible_suffix(const AttnParams& p, int64_t s, in
 }
 
 // Launches the tensor-core kernel over every unit of the plan (bf16).  With `direct`, every row
-// has exactly one partial result and suffix buffers hold at most kDirectSuffix tokens: the kernel adds
-// the row's own keys and writes out and lse instead.
-constexpr int kDirectSuffix = 4;
+// has exactly one partial result and suffix buffers hold at most one token: the kernel adds
+// the row's own key and writes out and lse instead.
+constexpr int kDirectSuffix = 1;
 tr_status launch_prefix_tc(const AttnParams& p, bool direct, cudaStream_t st);
 // The fp32 kernel over every unit (of 64 or 16 rows).
 tr_status launch_prefix_f32(const AttnParams& p, int unit_rows, cudaStream_t st);

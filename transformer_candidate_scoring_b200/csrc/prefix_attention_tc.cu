@@ -66,7 +66,6 @@ static_assert(Smem<128>::BYTES <= 232448 && Smem<64>::BYTES <= 232448, "shared m
 struct TcParams {
   CUtensorMap kmap, vmap;
   AttnParams a;
-  bool direct;
 };
 
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {    // K-major, 128-byte swizzle
@@ -200,7 +199,7 @@ __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, cons
       }
       if (done && ++ks == L::NK) { ks = 0; kph ^= 1; }
     };
-    qk(0);
+    if (n_jobs > 0) qk(0);
     if (n_jobs > 1) qk(1);
     for (int i = 0; i < n_jobs && ok; ++i) {
       const int t = i & 1, k = i >> 1, step = two ? k : i;
@@ -251,8 +250,7 @@ struct Row {
   Unit x;
   int base, jobs;        // the tile's first row in the unit, its steps
   bool live, warp_live;
-  int64_t token;         // query token of the batch
-  int head;
+  int token, head;       // query token of the batch, head
 };
 __device__ __forceinline__ Row row_at(const AttnParams& p, int u, int t, int tid) {
   Row r;
@@ -262,17 +260,30 @@ __device__ __forceinline__ Row row_at(const AttnParams& p, int u, int t, int tid
   r.live = r.base + tid < r.x.rows;
   r.warp_live = r.base + (tid & ~31) < r.x.rows;
   const int G = p.d.n_head / p.d.n_kv_head, m = r.x.m0 + r.base + tid;     // row within (request, key head)
-  r.token = (int64_t)p.req[r.x.r].s0 * p.d.L_t + m / G;
+  r.token = p.req[r.x.r].s0 * p.d.L_t + m / G;
   r.head = r.x.hk * G + m % G;
   return r;
+}
+// Where a row's own key begins (and its value).
+__device__ __forceinline__ int64_t own_at(const AttnParams& p, const Row& r) {
+  return (int64_t)(r.token / p.d.L_t) * p.d.suffix_seq + (int64_t)r.x.hk * p.d.suffix_head;
+}
+// Asks for a row's own key and value to be brought to L2, a unit ahead of their use.
+__device__ __forceinline__ void ask_own(const AttnParams& p, const Row& r) {
+  if (!r.live || p.d.suffix_cap == 0) return;
+  const int64_t at = own_at(p, r);
+  for (int i = 0; i < p.d.d_head; i += 64) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(p.k_suffix) + at + i));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(p.v_suffix) + at + i));
+  }
 }
 // This thread's row of Q into the Q tile, eight 16-byte pieces in flight.
 template <int DH>
 __device__ __forceinline__ void fill_q(const AttnParams& p, const Row& r, uint32_t tile, int tid) {
   const int D = p.d.d_head;
-  const bool in = r.live && r.jobs > 0;
+  const bool in = r.live;
   const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                  (in ? r.token * p.d.q_token + (int64_t)r.head * D : 0));
+                                                  (in ? r.token * p.d.q_token + r.head * D : 0));
 #pragma unroll
   for (int i0 = 0; i0 < DH / 8; i0 += 8) {
     uint4 v[8];
@@ -286,7 +297,7 @@ __device__ __forceinline__ void fill_q(const AttnParams& p, const Row& r, uint32
 
 // A softmax warpgroup (tile t): turns S into P step by step and writes the result.  The Q rows of its next
 // unit are on their way while this one's result is written.
-template <int DH>
+template <int DH, bool kDirect>
 __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t smem, float* sml, const Bars& b,
                              volatile int* abort_flag) {
   using L = Smem<DH>;
@@ -302,6 +313,7 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
   bool ok = true;
   Row next = row_at(p, blockIdx.x, t, tid);
   fill_q<DH>(p, next, q_tile, tid);
+  if (kDirect) ask_own(p, next);
   for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
     const Row rw = next;
     const Unit& x = rw.x;
@@ -400,22 +412,20 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
       l += a0 + a1;
     }
     if (!ok) break;
-    // ---- with `direct`, the row's own few keys: their scores, from the Q row in shared memory
-    const int64_t seq = rw.token / p.d.L_t;
-    const int64_t own = seq * p.d.suffix_seq + (int64_t)x.hk * p.d.suffix_head;
-    float a[kDirectSuffix];
-    int n_own = 0, n_warp = 0;
-    const bool writes = warp_live && (x.two || t == 0);
-    if (writes && tp.direct && p.d.suffix_cap > 0) {
-      n_own = live ? visible_suffix(p, seq, (int)(rw.token - seq * p.d.L_t)) : 0;
-      n_warp = __reduce_max_sync(0xffffffffu, n_own);
-#pragma unroll
-      for (int j = 0; j < kDirectSuffix; ++j) {
-        a[j] = -INFINITY;
-        if (j < n_own) {
-          const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_suffix) + own + j * p.d.suffix_token);
+    // ---- with kDirect, the row's own key: its score, from the Q row in shared memory
+    bool own = false;
+    float a = -INFINITY;
+    const uint4* own_v = nullptr;
+    if constexpr (kDirect) {
+      if (warp_live && (x.two || t == 0) && p.d.suffix_cap > 0) {
+        const int seq = rw.token / p.d.L_t;
+        own = live && visible_suffix(p, seq, rw.token - seq * p.d.L_t) > 0;
+        const int64_t at = own_at(p, rw);
+        own_v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_suffix) + at);
+        if (own) {
+          const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_suffix) + at);
           float acc = 0.f;
-#pragma unroll 2
+#pragma unroll 8
           for (int i = 0; i < D / 8; ++i) {
             const uint4 kv = __ldg(kr + i);
             uint4 qv;
@@ -424,11 +434,10 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
                          : "r"(piece(q_tile, tid, i)));
             acc = dot2(qv.x, kv.x, dot2(qv.y, kv.y, dot2(qv.z, kv.z, dot2(qv.w, kv.w, acc))));
           }
-          a[j] = acc * c;
+          a = acc * c;
         }
       }
     }
-    // ---- the next unit's Q sets out
     const bool more = u + gridDim.x < p.n_units;
     if (more) next = row_at(p, u + gridDim.x, t, tid);
     // ---- the result of the unit's rows
@@ -459,32 +468,31 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
       tc_fence_after();
       const bool second = !x.two && x.steps > 1;             // tile 1 has an O
       if (warp_live) {
-        const int64_t row = rw.token * p.d.n_head + rw.head;
+        const int64_t row = (int64_t)rw.token * p.d.n_head + rw.head;
         float ref = __fmul_rn(mref, c);
-        if (n_warp > 0) {
-          float top = ref;
-#pragma unroll
-          for (int j = 0; j < kDirectSuffix; ++j) top = fmaxf(top, a[j]);
-          const float tb = top == -INFINITY ? 0.f : top, f = ref == top ? 1.f : ex2(ref - tb);
-          lsum *= f;
+        if (kDirect && own) {
+          const float top = fmaxf(ref, a), tb = top == -INFINITY ? 0.f : top, f = ref == top ? 1.f : ex2(ref - tb);
+          a = ex2(a - tb);
+          lsum = lsum * f + a;
           w0 *= f;
           w1 *= f;
-#pragma unroll
-          for (int j = 0; j < kDirectSuffix; ++j) {
-            a[j] = ex2(a[j] - tb);
-            lsum += a[j];
-          }
           ref = top;
+        } else {
+          a = 0.f;
         }
         const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
         const float lse2 = lsum == 0.f ? -INFINITY : ref + log2f(lsum);
         const int64_t part = rq.part + x.split * request_rows(p, x.r) + (row - (int64_t)rq.s0 * p.d.L_t * p.d.n_head);
         w0 *= inv;
         w1 *= inv;
-#pragma unroll
-        for (int j = 0; j < kDirectSuffix; ++j) a[j] *= inv;
+        a *= inv;
 #pragma unroll 2
         for (int i = 0; i < (D + 15) / 16; ++i) {
+          uint4 v[2];
+          if constexpr (kDirect) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[h] = own && 16 * i + 8 * h < D ? __ldg(own_v + 2 * i + h) : make_uint4(0, 0, 0, 0);
+          }
           float o[16], o1[16];
           tmem_ld16(o_addr + 16 * i, o);
           if (second) tmem_ld16(o_addr + 128 + 16 * i, o1);
@@ -492,21 +500,16 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
           reg_fence<16>(o);
           reg_fence<16>(o1);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = second ? o[e] * w0 + o1[e] * w1 : o[e] * w0;
-          if (n_warp > 0) {
+          for (int e = 0; e < 16; ++e) o[e] = x.steps == 0 ? 0.f : second ? o[e] * w0 + o1[e] * w1 : o[e] * w0;
+          if constexpr (kDirect) {
 #pragma unroll
-            for (int j = 0; j < kDirectSuffix; ++j) {
-              const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_suffix) + own + j * p.d.suffix_token) + 2 * i;
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t vw[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+              if (own)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (j < n_own && 16 * i + 8 * h < D) {
-                  const uint4 v = __ldg(vr + h);
-                  const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    o[8 * h + 2 * e] = fmaf(a[j], __uint_as_float(vw[e] << 16), o[8 * h + 2 * e]);
-                    o[8 * h + 2 * e + 1] = fmaf(a[j], __uint_as_float(vw[e] & 0xFFFF0000u), o[8 * h + 2 * e + 1]);
-                  }
+                for (int e = 0; e < 4; ++e) {
+                  o[8 * h + 2 * e] = fmaf(a, __uint_as_float(vw[e] << 16), o[8 * h + 2 * e]);
+                  o[8 * h + 2 * e + 1] = fmaf(a, __uint_as_float(vw[e] & 0xFFFF0000u), o[8 * h + 2 * e + 1]);
                 }
             }
           }
@@ -514,7 +517,7 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               if (16 * i + 8 * h < D) {
-                if (tp.direct) {
+                if (kDirect) {
                   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D + 16 * i + 8 * h) =
                       make_uint4(pack_bf16(o[8 * h], o[8 * h + 1]), pack_bf16(o[8 * h + 2], o[8 * h + 3]),
                                  pack_bf16(o[8 * h + 4], o[8 * h + 5]), pack_bf16(o[8 * h + 6], o[8 * h + 7]));
@@ -527,7 +530,7 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
           }
         }
         if (live) {
-          if (!tp.direct)
+          if (!kDirect)
             p.part_lse[part] = lse2;
           else if (p.lse)
             p.lse[row] = lse2 * kLn2;
@@ -536,11 +539,14 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
       tc_fence_before();
       if (!x.two) mbar_arrive(b.ml_empty);
     }
-    if (more) fill_q<DH>(p, next, q_tile, tid);
+    if (more) {
+      fill_q<DH>(p, next, q_tile, tid);
+      if (kDirect) ask_own(p, next);
+    }
   }
 }
 
-template <int DH>
+template <int DH, bool kDirect>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ TcParams p) {
   using L = Smem<DH>;
   extern __shared__ uint8_t raw[];
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_tile<DH>(p, warp >> 2, tmem, smem, reinterpret_cast<float*>(gbase + L::ML), b, abort_flag);
+    softmax_tile<DH, kDirect>(p, warp >> 2, tmem, smem, reinterpret_cast<float*>(gbase + L::ML), b, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -617,9 +623,11 @@ tr_status encode_map(CUtensorMap* map, const void* base, const AttnParams& p) {
   auto encode = get_encode();
   if (!encode) return fail(TR_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const int64_t row = p.d.d_head;
+  const int tokens = std::max(p.req[p.R].p0, 1);
+  if (p.req[p.R].p0 == p.req[0].p0) base = p.q;            // no prefix at all: a map that nothing is read by
   // a dimension of one entry may come with any stride: it is never multiplied
-  const int64_t hs = p.d.n_kv_head > 1 ? p.d.prefix_head : row, ts = p.req[p.R].p0 > 1 ? p.d.prefix_token : row;
-  cuuint64_t gdim[3] = {(cuuint64_t)row, (cuuint64_t)p.d.n_kv_head, (cuuint64_t)p.req[p.R].p0};
+  const int64_t hs = p.d.n_kv_head > 1 ? p.d.prefix_head : row, ts = tokens > 1 ? p.d.prefix_token : row;
+  cuuint64_t gdim[3] = {(cuuint64_t)row, (cuuint64_t)p.d.n_kv_head, (cuuint64_t)tokens};
   cuuint64_t gstride[2] = {(cuuint64_t)hs * 2, (cuuint64_t)ts * 2};
   cuuint32_t box[3] = {64, 1, 128};
   cuuint32_t estride[3] = {1, 1, 1};
@@ -630,10 +638,10 @@ tr_status encode_map(CUtensorMap* map, const void* base, const AttnParams& p) {
   return TR_OK;
 }
 
-template <int DH>
+template <int DH, bool kDirect>
 tr_status launch(const TcParams& p, int sms, cudaStream_t st) {
-  TR_TRY(ensure_smem_attr((const void*)prefix_kernel<DH>, Smem<DH>::BYTES));
-  prefix_kernel<DH><<<std::min(p.a.n_units, sms), kThreads, Smem<DH>::BYTES, st>>>(p);
+  TR_TRY(ensure_smem_attr((const void*)prefix_kernel<DH, kDirect>, Smem<DH>::BYTES));
+  prefix_kernel<DH, kDirect><<<std::min(p.a.n_units, sms), kThreads, Smem<DH>::BYTES, st>>>(p);
   TR_LAUNCH_CHECK("prefix_kernel");
   return TR_OK;
 }
@@ -644,12 +652,12 @@ tr_status launch_prefix_tc(const AttnParams& a, bool direct, cudaStream_t st) {
   TcParams p;
   memset(&p, 0, sizeof p);
   p.a = a;
-  p.direct = direct;
   TR_TRY(encode_map(&p.kmap, a.k_prefix, a));
   TR_TRY(encode_map(&p.vmap, a.v_prefix, a));
   int sms = 0;
   TR_TRY(sm_count(&sms));
-  return a.d.d_head <= 64 ? launch<64>(p, sms, st) : launch<128>(p, sms, st);
+  if (direct) return a.d.d_head <= 64 ? launch<64, true>(p, sms, st) : launch<128, true>(p, sms, st);
+  return a.d.d_head <= 64 ? launch<64, false>(p, sms, st) : launch<128, false>(p, sms, st);
 }
 
 }  // namespace attn
