@@ -471,6 +471,9 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool dir
     q.chunk = best;
     q.n_split = ceil_div(steps[r], best);
     if (direct && best >= longest && q.s1 > q.s0) q.n_split = 1;
+    q.n_m = n_m[r];
+    q.div_m = fast_div_by((uint32_t)std::max(q.n_m, 1));
+    q.div_split = fast_div_by((uint32_t)std::max(q.n_split, 1));
     q.part = part;
     unit += p.d.n_kv_head * n_m[r] * q.n_split;
     part += request_rows(p, r) * q.n_split;
@@ -489,6 +492,8 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
   p.d = *d;
   p.R = R;
   p.n_rows = seq[R] * d->L_t * d->n_head;
+  p.div_g = fast_div_by((uint32_t)(d->n_head / d->n_kv_head));
+  p.div_lt = fast_div_by((uint32_t)d->L_t);
   for (int r = 0; r <= R; ++r) {
     RequestPlan& q = p.req[r];
     q.s0 = (int)seq[r];

@@ -18,6 +18,21 @@ constexpr int kStepKeysF32 = 64;
 // The prefix part of one request: rows = sequences x query tokens x heads of a key head.  A unit
 // is up to `unit_rows` of them of one key head over `chunk` steps of keys; a prefix of several chunks
 // gives each row several partial results.
+// n / d for 0 <= n < 2^31 as a multiplication: (mulhi(n, mul) + n) >> shift, after Granlund and Montgomery,
+// "Division by Invariant Integers using Multiplication".
+struct FastDiv {
+  uint32_t mul = 1, shift = 0;
+};
+inline FastDiv fast_div_by(uint32_t d) {       // 1 <= d < 2^31
+  FastDiv f;
+  while ((1ull << f.shift) < d) ++f.shift;
+  f.mul = (uint32_t)((((1ull << f.shift) - d) << 32) / d + 1);
+  return f;
+}
+__device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
+  return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift);
+}
+
 struct RequestPlan {
   int first_unit;      // units of request r: first_unit[r] .. first_unit[r+1]-1
   int n_split;         // chunks of the prefix (0: no prefix or no sequences)
@@ -25,6 +40,8 @@ struct RequestPlan {
   int p0, p1;          // prefix tokens
   int s0, s1;          // sequences
   int64_t part;        // the request's first partial result
+  int n_m;             // units of rows per key head and chunk
+  FastDiv div_m, div_split;
 };
 
 struct AttnParams {
@@ -36,6 +53,7 @@ struct AttnParams {
   tr_attn_desc d;
   int R, n_units;
   int64_t n_rows;      // query rows of all requests: n * L_t * n_head
+  FastDiv div_g, div_lt;   // by n_head / n_kv_head, by L_t
   // partial result i of row `row` of request r (its rows counted from 0, head fastest) is
   // part_o[(part + i * rows of r + row) * d_head ..] and part_lse[the same] (times log2 e)
   float *part_o, *part_lse;
@@ -63,14 +81,12 @@ __device__ __forceinline__ Unit unit_at(const AttnParams& p, int u, int unit_row
   }
   const RequestPlan& q = p.req[lo];
   const int m_all = (q.s1 - q.s0) * p.d.L_t * (p.d.n_head / p.d.n_kv_head);
-  const int n_m = (m_all + unit_rows - 1) / unit_rows;
-  int i = u - q.first_unit;
+  const int i = u - q.first_unit, im = fast_div(i, q.div_m);
   Unit x;
   x.r = lo;
-  x.m0 = (i % n_m) * unit_rows;      // units that share keys are neighbours
-  i /= n_m;
-  x.split = i % q.n_split;
-  x.hk = i / q.n_split;
+  x.m0 = (i - im * q.n_m) * unit_rows;      // units that share keys are neighbours
+  x.hk = fast_div(im, q.div_split);
+  x.split = im - x.hk * q.n_split;
   x.rows = min(unit_rows, m_all - x.m0);
   x.two = x.rows > unit_rows / 2;
   const int k0 = x.split * q.chunk * step_keys;

@@ -260,13 +260,14 @@ __device__ __forceinline__ Row row_at(const AttnParams& p, int u, int t, int tid
   r.live = r.base + tid < r.x.rows;
   r.warp_live = r.base + (tid & ~31) < r.x.rows;
   const int G = p.d.n_head / p.d.n_kv_head, m = r.x.m0 + r.base + tid;     // row within (request, key head)
-  r.token = p.req[r.x.r].s0 * p.d.L_t + m / G;
-  r.head = r.x.hk * G + m % G;
+  const int tok = fast_div(m, p.div_g);
+  r.token = p.req[r.x.r].s0 * p.d.L_t + tok;
+  r.head = r.x.hk * G + m - tok * G;
   return r;
 }
 // Where a row's own key begins (and its value).
 __device__ __forceinline__ int64_t own_at(const AttnParams& p, const Row& r) {
-  return (int64_t)(r.token / p.d.L_t) * p.d.suffix_seq + (int64_t)r.x.hk * p.d.suffix_head;
+  return (int64_t)fast_div(r.token, p.div_lt) * p.d.suffix_seq + (int64_t)r.x.hk * p.d.suffix_head;
 }
 // Asks for a row's own key and value to be brought to L2, a unit ahead of their use.
 __device__ __forceinline__ void ask_own(const AttnParams& p, const Row& r) {
@@ -341,8 +342,12 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
         reg_fence<kN>(s);
         if (valid < kN) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i)
-            if (i >= valid) s[i] = -INFINITY;
+          for (int i = 0; i < kN; i += 32)
+            if (i + 32 > valid) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (i + e >= valid) s[i + e] = -INFINITY;
+            }
         }
         float n0 = mx, n1 = s[0], n2 = s[1], n3 = s[2];
 #pragma unroll
@@ -418,7 +423,7 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
     const uint4* own_v = nullptr;
     if constexpr (kDirect) {
       if (warp_live && (x.two || t == 0) && p.d.suffix_cap > 0) {
-        const int seq = rw.token / p.d.L_t;
+        const int seq = fast_div(rw.token, p.div_lt);
         own = live && visible_suffix(p, seq, rw.token - seq * p.d.L_t) > 0;
         const int64_t at = own_at(p, rw);
         own_v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_suffix) + at);
