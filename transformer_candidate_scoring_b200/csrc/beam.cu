@@ -795,7 +795,7 @@ tr_status launch_select(const SelectParams& p, int R, uintptr_t align, cudaStrea
   TR_LAUNCH_CHECK("beam_sum_kernel");
   constexpr int kPickBytes = kPickCap * (sizeof(Rank) + sizeof(int));
   TR_TRY(ensure_smem_attr((const void*)beam_pick_kernel<T>, kPickBytes));
-  return launch_dependent(beam_pick_kernel<T>, (unsigned)R, kPickThreads, kPickBytes, st, "beam_pick_kernel", p);
+  return launch_dependent(true, beam_pick_kernel<T>, (unsigned)R, kPickThreads, kPickBytes, st, "beam_pick_kernel", p);
 }
 
 tr_status check_select(int R, int W, int V, int k) {

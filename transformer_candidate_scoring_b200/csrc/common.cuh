@@ -61,10 +61,12 @@ tr_status ensure_smem_attr(const void* kernel, int bytes);
 // SMs of the current device.
 tr_status sm_count(int* out);
 
-// Launches a kernel that may start before the one launched last on the stream has ended: it calls
-// cudaGridDependencySynchronize() before it touches anything that kernel writes.
+// Launches a kernel that, with `early`, may start before the one launched last on the stream has ended.  That
+// one has to be the library's own, launched in the same call: the kernel reads the call's inputs at once (what
+// wrote them ended before the other began) and calls cudaGridDependencySynchronize() before it touches
+// anything that the other writes.
 template <typename... Params, typename... Args>
-tr_status launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+tr_status launch_dependent(bool early, void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
                            const char* what, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -75,7 +77,7 @@ tr_status launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned th
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   count_launch();
   if (e != cudaSuccess) return fail(TR_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));

@@ -213,7 +213,7 @@ tr_status launch_finish(const AttnParams& p, int sms, cudaStream_t st) {
          p.n_rows * kLanes * parts * 2 <= (int64_t)sms * 16 * 32)
     parts *= 2;
   const int rows_per = kFinishThreads / kLanes / parts;
-  return launch_dependent(finish_kernel<T, kLanes>, (unsigned)((p.n_rows + rows_per - 1) / rows_per), kFinishThreads, 0, st,
+  return launch_dependent(p.n_units > 0, finish_kernel<T, kLanes>, (unsigned)((p.n_rows + rows_per - 1) / rows_per), kFinishThreads, 0, st,
                           "finish_kernel", p, parts);
 }
 template <typename T>
@@ -383,7 +383,7 @@ tr_status launch_suffix(const AttnParams& p, cudaStream_t st) {
   const int steps = (p.d.suffix_cap + 15) / 16, parts = steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
   const int r_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 7) / 8, units = kSuffixThreads / 32 / parts;
   const int64_t n_unit = (int64_t)p.req[p.R].s0 * p.d.n_kv_head * r_tiles;
-  return launch_dependent(suffix_kernel<kBlocks>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
+  return launch_dependent(p.n_units > 0, suffix_kernel<kBlocks>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
                           parts, r_tiles);
 }
 
