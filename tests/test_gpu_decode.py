@@ -191,6 +191,47 @@ def test_attention_ignores_values_behind_prefix_and_suffix(api, dtype, bad):
         agrees(got, part, d ** -0.5, False)
 
 
+@pytest.mark.parametrize("d", [64, 104])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_causal_rows_ignore_later_values(api, dtype, bad, d):
+    """The values of a sequence's last two tokens hold NaN or infinities: the query tokens before
+    them get what they get without, the others what the formula gives."""
+    x = attn_inputs(16, [2, 3], [20, 0], 6, 2, d, 40, 5, dtype, lens=[40, 33, 9, 2, 17])
+    y = dict(x, vs=x["vs"].clone())
+    for s in range(5):
+        y["vs"][s, max(0, int(x["sl"][s]) - 2):int(x["sl"][s])] = bad
+    clean, got = (call(api, dev(z), causal=True) for z in (x, y))
+    ok(api)
+    agrees(clean, x, d ** -0.5, True)
+    agrees((got[0][:, :3], got[1][:, :3]), dict(x, q=x["q"][:, :3], sl=(x["sl"] - 2).clamp(min=0)), d ** -0.5, True)
+    late = got[0][:, 3:].float()
+    assert bool((torch.isnan(late) if bad != bad else late == bad).all())
+    assert torch.equal(got[1], clean[1])                    # scores do not read values
+
+
+RAGGED = [5003, 1, 700, 2049, 4100, 128, 127, 5990, 3333, 129, 64, 2500, 1111, 5500, 900, 0, 4999, 2222]
+RUNS = [
+    # counts, prefix, H, H_kv, d, S, L_t, causal
+    ([1 + i % 2 for i in range(18)], RAGGED, 8, 8, 64, 3, 1, False),
+    ([1 + i % 2 for i in range(17)] + [0], RAGGED, 16, 8, 128, 9, 1, False),
+    ([1 + i % 2 for i in range(18)], RAGGED, 10, 10, 32, 0, 1, False),
+    ([1 + i % 2 for i in range(17)] + [35], RAGGED, 16, 8, 96, 1, 2, True),      # of the last, two tiles of rows
+]
+
+
+@pytest.mark.parametrize("case", RUNS, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}x{c[3]}x{c[4]}".replace(" ", ""))
+def test_attention_ragged_long_prefixes(api, case):
+    """Prefixes of very different lengths for few rows each: their keys are shared out by equal runs."""
+    counts, prefix, H, H_kv, d, S, L_t, causal = case
+    x = attn_inputs(17, counts, prefix, H, H_kv, d, S, L_t)
+    got = call(api, dev(x), causal=causal)
+    again = call(api, dev(x), causal=causal)
+    ok(api)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    agrees(got, x, d ** -0.5, causal)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_neighbouring_prefixes_do_not_leak(api, dtype):
     """A request whose prefix holds NaN leaves the requests before and after it untouched."""

@@ -68,21 +68,24 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&y);
 }
-// Joins the prefix part's results part, part + parts, ... of a row (the first at at0, the next `rows`
+__device__ __forceinline__ bool not_finite(uint32_t w) {       // either of two bf16
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+// Joins the prefix part's results part, part + parts, ... of a row's n (the first at at0, the next `rows`
 // further) for columns c0 .. c0 + 7, four at a time.
-__device__ __forceinline__ void merge_prefix(const AttnParams& p, const RequestPlan& rq, int64_t at0, int64_t rows, int c0, bool in,
+__device__ __forceinline__ void merge_prefix(const AttnParams& p, int n, int64_t at0, int64_t rows, int c0, bool in,
                                              int part, int parts, Running& x) {
   const int D = p.d.d_head;
   constexpr int kAhead = 4;
-  for (int i0 = part; i0 < rq.n_split; i0 += parts * kAhead) {
+  for (int i0 = part; i0 < n; i0 += parts * kAhead) {
     float z[kAhead], oo[kAhead][8];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = i0 + u * parts;
-      z[u] = i < rq.n_split ? p.part_lse[at0 + i * rows] : -INFINITY;
+      z[u] = i < n ? p.part_lse[at0 + i * rows] : -INFINITY;
 #pragma unroll
       for (int e = 0; e < 8; ++e) oo[u][e] = 0.f;
-      if (in && i < rq.n_split) {
+      if (in && i < n) {
         const float4* y = reinterpret_cast<const float4*>(p.part_o + (at0 + i * rows) * D + c0);
         const float4 f = y[0], g = y[1];
         oo[u][0] = f.x; oo[u][1] = f.y; oo[u][2] = f.z; oo[u][3] = f.w;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   cudaGridDependencySynchronize();
   const int64_t rows = (int64_t)(rq.s1 - rq.s0) * p.d.L_t * H;
   const int64_t at0 = rq.part + (row - (int64_t)rq.s0 * p.d.L_t * H);
-  merge_prefix(p, rq, at0, rows, c0, in, part, parts, x);
+  merge_prefix(p, results_of(p, rq), at0, rows, c0, in, part, parts, x);
   if (parts > 1) {
     if (tl == 0) {
       s_ml[team][0] = x.m;
@@ -248,7 +251,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   return r;
 }
 
-template <int kBlocks>     // 64-wide blocks of d_head
+template <int kBlocks, bool kCausal>     // 64-wide blocks of d_head
 __global__ void __launch_bounds__(kSuffixThreads, kBlocks == 1 ? 6 : 4)
 suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
   constexpr int DP = kBlocks * 64;
@@ -276,7 +279,8 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
   int seen[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
-    seen[e] = p.d.causal ? max(0, len - max(0, p.d.L_t - 1 - (row0 + 2 * qd + e) / G)) : len;
+    seen[e] = kCausal ? max(0, len - max(0, p.d.L_t - 1 - (row0 + 2 * qd + e) / G)) : len;
+  const int seen_by_all = kCausal ? max(0, len - (p.d.L_t - 1 - row0 / G)) : len;
   const int64_t so = (int64_t)s * p.d.suffix_seq + hk * p.d.suffix_head;
   const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(p.k_suffix) + so, *vp = static_cast<const __nv_bfloat16*>(p.v_suffix) + so;
   float o[4 * kBlocks][4] = {};                            // O^T: 16 columns of d_head x 8 rows
@@ -319,6 +323,37 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
       st[2 + e] = exp2f(a1 - base);
       l[e] = l[e] * f[e] + st[e] + st[2 + e];              // (this lane's keys only)
     }
+    // Of keys that only the later of the rows see, the product's 0 x V of the others is 0 unless V is
+    // infinite or NaN: then every row adds the keys it sees, one by one.
+    if (kCausal && j0 + 16 > seen_by_all && len > seen_by_all) {
+      bool odd = false;
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) odd = odd || not_finite(v[h][b].x) || not_finite(v[h][b].y) || not_finite(v[h][b].z) || not_finite(v[h][b].w);
+      if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+        for (int i = 0; i < 4 * kBlocks; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= f[e & 1];
+        for (int jj = 0; jj < 16 && j0 + jj < len; ++jj) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) w[e] = __shfl_sync(0xffffffffu, jj < 8 ? st[e] : st[2 + e], (jj & 7) * 4 + qd);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            float y[8] = {};
+            if (b * 64 + g * 8 < D) load8(vp + (j0 + jj) * p.d.suffix_token + b * 64 + g * 8, y);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (j0 + jj < seen[e])
+#pragma unroll
+                for (int x = 0; x < 8; ++x) o[4 * b + x / 2][2 * (x & 1) + e] = fmaf(w[e], y[x], o[4 * b + x / 2][2 * (x & 1) + e]);
+          }
+        }
+        continue;
+      }
+    }
     const uint32_t b0 = transpose_8x8(bf16x2(st[0], st[1])), b1 = transpose_8x8(bf16x2(st[2], st[3]));
 #pragma unroll
     for (int i = 0; i < 4 * kBlocks; ++i) {
@@ -355,7 +390,7 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
   if (u_at >= n_unit) return;
   const RequestPlan& rq = p.req[request_of(p, s)];
   const int64_t rows = (int64_t)(rq.s1 - rq.s0) * p.d.L_t * H;
-  const int chunks = D / 8, first = warp / parts * parts;
+  const int chunks = D / 8, first = warp / parts * parts, n_results = results_of(p, rq);
   for (int item = part * 32 + lane; item < min(8, n_rows - row0) * chunks; item += parts * 32) {
     const int rr = item / chunks, c0 = item % chunks * 8, r = row0 + rr;
     const int64_t row = ((int64_t)s * p.d.L_t + r / G) * H + hk * G + r % G;
@@ -371,19 +406,19 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x.o[e] = fmaf(f, w[e], x.o[e]);
     }
-    merge_prefix(p, rq, rq.part + (row - (int64_t)rq.s0 * p.d.L_t * H), rows, c0, true, 0, 1, x);
+    merge_prefix(p, n_results, rq.part + (row - (int64_t)rq.s0 * p.d.L_t * H), rows, c0, true, 0, 1, x);
     store_row<__nv_bfloat16>(p, row, c0, x);
     if (p.lse && c0 == 0) p.lse[row] = x.lse();
   }
 }
 
-template <int kBlocks>
+template <int kBlocks, bool kCausal>
 tr_status launch_suffix(const AttnParams& p, cudaStream_t st) {
   // a warp per 16 keys up to the four of a CTA
   const int steps = (p.d.suffix_cap + 15) / 16, parts = steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
   const int r_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 7) / 8, units = kSuffixThreads / 32 / parts;
   const int64_t n_unit = (int64_t)p.req[p.R].s0 * p.d.n_kv_head * r_tiles;
-  return launch_dependent(p.n_units > 0, suffix_kernel<kBlocks>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
+  return launch_dependent(p.n_units > 0, suffix_kernel<kBlocks, kCausal>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
                           parts, r_tiles);
 }
 
@@ -422,7 +457,8 @@ tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t
 // result) and every chunk of a prefix a partial result per row.  The candidates are: no split, and
 // the shortest chunks that give one, two or four units per slot.  With `direct`, no split also saves the
 // merge's launch (about 4 us), and requests without a prefix have one (empty) unit per 256 rows.
-void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool direct) {
+// With `runs`, equal runs of steps are a candidate too, at a unit more per CTA.
+void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool direct, bool runs) {
   const int G = p.d.n_head / p.d.n_kv_head;
   int steps[TR_MAX_REQUESTS], n_m[TR_MAX_REQUESTS];
   int longest = 0;
@@ -463,22 +499,37 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool dir
       best = c;
     }
   }
+  if (runs && longest > 0 && p.d.n_kv_head <= slots && *std::max_element(n_m, n_m + p.R) == 1) {
+    int line = 0, filled = 0;                 // (below 2^24 + R steps)
+    for (int r = 0; r < p.R; ++r) line += steps[r], filled += steps[r] > 0;
+    const int run = ceil_div(line, slots / p.d.n_kv_head), n = ceil_div(line, run);
+    const double split = 1.0 + (double)line / ((double)run * filled);
+    const double cost = run * (two ? 2.0 : 1.0) + 3.0 * (n + filled) / n + (double)rows_all * split * p.d.d_head * 8.0 / 3.5e6 +
+                        (direct ? 6.0 : 0.0);
+    if (cost < best_cost) {
+      p.run = run;
+      p.div_run = fast_div_by((uint32_t)run);
+      p.n_units = n * p.d.n_kv_head;
+    }
+  }
   int unit = 0;
   int64_t part = 0;
   for (int r = 0; r < p.R; ++r) {
     RequestPlan& q = p.req[r];
     q.first_unit = unit;
-    q.chunk = best;
-    q.n_split = ceil_div(steps[r], best);
-    if (direct && best >= longest && q.s1 > q.s0) q.n_split = 1;
+    q.chunk = p.run > 0 ? steps[r] : best;
+    // (a line of n steps meets at most ceil(n / run) + 1 runs)
+    q.n_split = p.run > 0 ? (steps[r] > 0 ? ceil_div(steps[r], p.run) + 1 : 0) : ceil_div(steps[r], best);
+    if (direct && p.run == 0 && best >= longest && q.s1 > q.s0) q.n_split = 1;
     q.n_m = n_m[r];
     q.div_m = fast_div_by((uint32_t)std::max(q.n_m, 1));
     q.div_split = fast_div_by((uint32_t)std::max(q.n_split, 1));
     q.part = part;
-    unit += p.d.n_kv_head * n_m[r] * q.n_split;
+    unit += p.run > 0 ? steps[r] : p.d.n_kv_head * n_m[r] * q.n_split;
     part += request_rows(p, r) * q.n_split;
   }
-  p.req[p.R].first_unit = p.n_units = unit;
+  p.req[p.R].first_unit = unit;
+  if (p.run == 0) p.n_units = unit;
   p.req[p.R].part = part;
 }
 
@@ -494,6 +545,7 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
   p.n_rows = seq[R] * d->L_t * d->n_head;
   p.div_g = fast_div_by((uint32_t)(d->n_head / d->n_kv_head));
   p.div_lt = fast_div_by((uint32_t)d->L_t);
+  p.div_kv = fast_div_by((uint32_t)d->n_kv_head);
   for (int r = 0; r <= R; ++r) {
     RequestPlan& q = p.req[r];
     q.s0 = (int)seq[r];
@@ -508,13 +560,13 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
     int64_t most = 0;
     for (int r = 0; r < R; ++r) most = std::max(most, (seq[r + 1] - seq[r]) * d->L_t * (d->n_head / d->n_kv_head));
     plan.unit_rows = most <= 32 ? 16 : 64;
-    plan_units(p, plan.unit_rows, kStepKeysF32, 2 * plan.sms, false);
+    plan_units(p, plan.unit_rows, kStepKeysF32, 2 * plan.sms, false, false);
     plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);
     return TR_OK;
   }
   plan.unit_rows = kUnitRows;
-  plan_units(p, kUnitRows, kStepKeys, plan.sms, d->suffix_cap <= kDirectSuffix);
-  plan.direct = d->suffix_cap <= kDirectSuffix;
+  plan_units(p, kUnitRows, kStepKeys, plan.sms, d->suffix_cap <= kDirectSuffix, true);
+  plan.direct = d->suffix_cap <= kDirectSuffix && p.run == 0;
   for (int r = 0; r < R; ++r) plan.direct = plan.direct && (p.req[r].n_split == 1 || p.req[r].s0 == p.req[r].s1);
   if (!plan.direct) plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);
   return TR_OK;
@@ -575,6 +627,9 @@ extern "C" tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q
   }
   if (p.n_units > 0) TR_TRY(launch_prefix_tc(p, plan.direct, st));
   if (plan.direct) return TR_OK;
-  if (desc->suffix_cap >= 8) return desc->d_head <= 64 ? launch_suffix<1>(p, st) : launch_suffix<2>(p, st);
+  if (desc->suffix_cap >= 8) {
+    if (desc->d_head <= 64) return desc->causal ? launch_suffix<1, true>(p, st) : launch_suffix<1, false>(p, st);
+    return desc->causal ? launch_suffix<2, true>(p, st) : launch_suffix<2, false>(p, st);
+  }
   return launch_finish<__nv_bfloat16>(p, plan.sms, st);
 }

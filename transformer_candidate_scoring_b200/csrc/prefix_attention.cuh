@@ -18,6 +18,12 @@ constexpr int kStepKeysF32 = 64;
 // The prefix part of one request: rows = sequences x query tokens x heads of a key head.  A unit
 // is up to `unit_rows` of them of one key head over `chunk` steps of keys; a prefix of several chunks
 // gives each row several partial results.
+//
+// Where no key head has more rows than a unit (each key is read by one CTA), the cut may be by runs
+// instead (`run` > 0): the steps of all requests stand in one line, of which a team of n_kv_head CTAs, one
+// per key head, takes `run`; a unit is what of a run belongs to one request.  However the prefixes' lengths
+// differ, every CTA has the same share, and a token's key heads, neighbours in memory, are read together.
+
 // n / d for 0 <= n < 2^31 as a multiplication: (mulhi(n, mul) + n) >> shift, after Granlund and Montgomery,
 // "Division by Invariant Integers using Multiplication".
 struct FastDiv {
@@ -34,9 +40,9 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
 }
 
 struct RequestPlan {
-  int first_unit;      // units of request r: first_unit[r] .. first_unit[r+1]-1
-  int n_split;         // chunks of the prefix (0: no prefix or no sequences)
-  int chunk;           // steps per chunk
+  int first_unit;      // units (with runs: steps) of request r: first_unit[r] .. first_unit[r+1]-1
+  int n_split;         // partial results per row, with runs at most (0: no prefix or no sequences)
+  int chunk;           // steps per chunk; with runs, of the prefix
   int p0, p1;          // prefix tokens
   int s0, s1;          // sequences
   int64_t part;        // the request's first partial result
@@ -51,9 +57,11 @@ struct AttnParams {
   float* lse;
   int* status;
   tr_attn_desc d;
-  int R, n_units;
+  int R, n_units;      // (with runs, the CTAs)
+  int run;             // steps per CTA, 0: units of `chunk` steps
   int64_t n_rows;      // query rows of all requests: n * L_t * n_head
   FastDiv div_g, div_lt;   // by n_head / n_kv_head, by L_t
+  FastDiv div_run, div_kv; // by run, by n_kv_head
   // partial result i of row `row` of request r (its rows counted from 0, head fastest) is
   // part_o[(part + i * rows of r + row) * d_head ..] and part_lse[the same] (times log2 e)
   float *part_o, *part_lse;
@@ -62,6 +70,12 @@ struct AttnParams {
 
 __host__ __device__ inline int64_t request_rows(const AttnParams& p, int r) {
   return (int64_t)(p.req[r].s1 - p.req[r].s0) * p.d.L_t * p.d.n_head;
+}
+
+// Partial results of a row of request q.
+__device__ __forceinline__ int results_of(const AttnParams& p, const RequestPlan& q) {
+  if (p.run == 0 || q.n_split == 0) return q.n_split;
+  return fast_div(q.first_unit + q.chunk - 1, p.div_run) - fast_div(q.first_unit, p.div_run) + 1;
 }
 
 struct Unit {
@@ -81,20 +95,37 @@ __device__ __forceinline__ Unit unit_at(const AttnParams& p, int u, int unit_row
   }
   const RequestPlan& q = p.req[lo];
   const int m_all = (q.s1 - q.s0) * p.d.L_t * (p.d.n_head / p.d.n_kv_head);
-  const int i = u - q.first_unit, im = fast_div(i, q.div_m);
+  const int i = u - q.first_unit;
   Unit x;
   x.r = lo;
-  x.m0 = (i - im * q.n_m) * unit_rows;      // units that share keys are neighbours
-  x.hk = fast_div(im, q.div_split);
-  x.split = im - x.hk * q.n_split;
+  if (p.run > 0) {
+    const int team = fast_div(blockIdx.x, p.div_kv);
+    x.hk = blockIdx.x - team * p.d.n_kv_head;
+    x.m0 = 0;
+    x.split = team - fast_div(q.first_unit, p.div_run);
+    x.tok = q.p0 + i * step_keys;
+    x.steps = min(q.chunk - i, (team + 1) * p.run - u);
+  } else {
+    const int im = fast_div(i, q.div_m);
+    x.m0 = (i - im * q.n_m) * unit_rows;      // units that share keys are neighbours
+    x.hk = fast_div(im, q.div_split);
+    x.split = im - x.hk * q.n_split;
+    x.tok = q.p0 + x.split * q.chunk * step_keys;
+    x.steps = q.chunk;
+  }
   x.rows = min(unit_rows, m_all - x.m0);
   x.two = x.rows > unit_rows / 2;
-  const int k0 = x.split * q.chunk * step_keys;
-  x.tok = q.p0 + k0;
-  x.keys = min(q.chunk * step_keys, q.p1 - x.tok);
+  x.keys = min(x.steps * step_keys, q.p1 - x.tok);
   x.steps = (x.keys + step_keys - 1) / step_keys;
   return x;
 }
+
+// The units of this CTA: for (u = first_of(p); u < end_of(p); u = after(p, u, the unit)).
+__device__ __forceinline__ int first_of(const AttnParams& p) { return p.run > 0 ? fast_div(blockIdx.x, p.div_kv) * p.run : blockIdx.x; }
+__device__ __forceinline__ int end_of(const AttnParams& p) {
+  return p.run > 0 ? min((fast_div(blockIdx.x, p.div_kv) + 1) * p.run, p.req[p.R].first_unit) : p.n_units;
+}
+__device__ __forceinline__ int after(const AttnParams& p, int u, const Unit& x) { return p.run > 0 ? u + x.steps : u + gridDim.x; }
 
 // Suffix keys that query token t of sequence s sees; a length outside the buffer is clamped.
 __device__ __forceinline__ int visible_suffix(const AttnParams& p, int64_t s, int t) {

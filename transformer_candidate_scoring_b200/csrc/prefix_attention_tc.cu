@@ -140,8 +140,10 @@ __device__ void load_steps(const AttnParams& p, const CUtensorMap* map, uint32_t
   uint32_t ph = 0;
   bool ok = true;
   uint32_t pending = 0, par = 0;           // bit s: a load of slot s was issued, and its parity
-  for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
+  const int end = end_of(p);
+  for (int u = first_of(p); u < end && ok;) {
     const Unit x = unit_at(p, u, kUnitRows, kN);
+    u = after(p, u, x);
     for (int j = 0; j < x.steps; ++j) {
       if (!(ok = mbar_wait_idle(empty + 8 * s, ph ^ 1, abort_flag))) break;
       const uint32_t dst = ring + s * Smem<DH>::TILE;
@@ -170,8 +172,10 @@ __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, cons
   int ks = 0, vs = 0;                                      // ring slots of the current step
   uint32_t kph = 0, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
   bool ok = true;
-  for (int u = blockIdx.x; u < p.a.n_units && ok; u += gridDim.x) {
+  const int end = end_of(p.a);
+  for (int u = first_of(p.a); u < end && ok;) {
     const Unit x = unit_at(p.a, u, kUnitRows, kN);
+    u = after(p.a, u, x);
     const bool two = x.two;
     const int n_jobs = two ? 2 * x.steps : x.steps;
     const int last = x.keys - (x.steps - 1) * kN;          // keys of the last step
@@ -312,10 +316,12 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
   const uint64_t c2 = f32x2(c, c);
   uint32_t sph = 0, oph = 0, xph = 0;
   bool ok = true;
-  Row next = row_at(p, blockIdx.x, t, tid);
+  const int end = end_of(p);
+  int u = first_of(p);
+  Row next = row_at(p, u, t, tid);
   fill_q<DH>(p, next, q_tile, tid);
   if (kDirect) ask_own(p, next);
-  for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
+  while (u < end && ok) {
     const Row rw = next;
     const Unit& x = rw.x;
     const RequestPlan& rq = p.req[x.r];
@@ -443,8 +449,9 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
         }
       }
     }
-    const bool more = u + gridDim.x < p.n_units;
-    if (more) next = row_at(p, u + gridDim.x, t, tid);
+    u = after(p, u, x);
+    const bool more = u < end;
+    if (more) next = row_at(p, u, t, tid);
     // ---- the result of the unit's rows
     if (jobs > 0) {
       if (!(ok = wait_all(b.odone + 8 * t, oph, abort_flag))) break;
