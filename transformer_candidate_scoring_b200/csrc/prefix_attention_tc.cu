@@ -57,7 +57,8 @@ template <int DH>    // d_head padded to 64 or 128
 struct Smem {
   static constexpr int TILE = 128 * DH * 2;
   static constexpr int NK = DH == 128 ? 3 : 4, NV = DH == 128 ? 2 : 4;
-  static constexpr int Q = 0, K = 2 * TILE, V = K + NK * TILE, BAR = V + NV * TILE;
+  static constexpr int NQ = DH == 128 ? 2 : 4;   // Q tiles
+  static constexpr int Q = 0, K = NQ * TILE, V = K + NK * TILE, BAR = V + NV * TILE;
   static constexpr int ML = BAR + 256;           // m and l of tile 1's rows (merge)
   static constexpr int BYTES = ML + 1024 + 1024;   // + alignment of the base
 };
@@ -126,9 +127,18 @@ __device__ __forceinline__ uint32_t piece(uint32_t tile, int r, int c) {
   return tile + r * 128 + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// Whether Q has two buffers, so that a unit's rows come while the one before it is worked on: d_head up to
+// 64, or units that all have one tile of rows (kOne).
+template <int DH, bool kOne>
+constexpr bool kQAhead = DH == 64 || kOne;
+// Bytes from one Q buffer to the other.
+template <int DH, bool kOne>
+constexpr uint32_t kQBuffer = (DH == 64 ? 2 : 1) * Smem<DH>::TILE;
+
 struct Bars {
   uint32_t kfull, kempty, vfull, vempty;   // rings, 8 bytes apart
-  uint32_t qfull, sfull, pfull, odone;     // per tile (pfull: two per tile)
+  uint32_t qfull, sfull, pfull, odone;     // per tile (pfull: two per tile; qfull: per buffer if there are two)
+  uint32_t qempty;                         // per buffer
   uint32_t ml_full, ml_empty;
 };
 
@@ -163,7 +173,7 @@ __device__ void load_steps(const AttnParams& p, const CUtensorMap* map, uint32_t
 }
 
 // The whole warp: one lane issues, all lanes zero V rows behind the prefix.
-template <int DH>
+template <int DH, bool kOne>
 __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, const Bars& b, int lane, volatile int* abort_flag) {
   using L = Smem<DH>;
   const int dk = (p.a.d.d_head + 15) / 16;                 // 16-wide slices of d_head
@@ -171,26 +181,28 @@ __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, cons
   const uint64_t q0 = desc_k(smem + L::Q), k0 = desc_k(smem + L::K), v0 = desc_mn(smem + L::V, 128 * 128);
   int ks = 0, vs = 0;                                      // ring slots of the current step
   uint32_t kph = 0, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+  constexpr bool kAhead = kQAhead<DH, kOne>;
+  int buf = 0;                                             // Q buffer
   bool ok = true;
   const int end = end_of(p.a);
   for (int u = first_of(p.a); u < end && ok;) {
     const Unit x = unit_at(p.a, u, kUnitRows, kN);
     u = after(p.a, u, x);
-    const bool two = x.two;
+    const bool two = !kOne && x.two;
     const int n_jobs = two ? 2 * x.steps : x.steps;
     const int last = x.keys - (x.steps - 1) * kN;          // keys of the last step
     auto qk = [&](int i) {
       const int t = i & 1, step = two ? i >> 1 : i;
-      if (i < 2) {
-        ok = ok && wait_all(b.qfull + 8 * t, qph[t], abort_flag);
-        qph[t] ^= 1;
+      if (i < (kAhead ? 1 : 2)) {
+        ok = ok && wait_all(b.qfull + 8 * (kAhead ? buf : t), qph[kAhead ? buf : t], abort_flag);
+        qph[kAhead ? buf : t] ^= 1;
       }
       ok = ok && wait_all(b.kfull + 8 * ks, kph, abort_flag);
       if (!ok) return;
       const bool done = !two || t == 1;                    // nothing reads these keys any more
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t qa = q0 + t * (L::TILE >> 4), ka = k0 + ks * (L::TILE >> 4);
+        const uint64_t qa = q0 + (kAhead ? buf * (kQBuffer<DH, kOne> >> 4) + (two ? t * (L::TILE >> 4) : 0) : t * (L::TILE >> 4)), ka = k0 + ks * (L::TILE >> 4);
         const uint32_t id = step == x.steps - 1 ? idesc_bf16(kM, (last + 15) & ~15) : id_full;
 #pragma unroll
         for (int kk = 0; kk < DH / 16; ++kk)
@@ -200,11 +212,17 @@ __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, cons
           }
         mma_commit(b.sfull + 8 * t);
         if (done) mma_commit(b.kempty + 8 * ks);
+        if (kAhead && i == n_jobs - 1) mma_commit(b.qempty + 8 * buf);
       }
       if (done && ++ks == L::NK) { ks = 0; kph ^= 1; }
     };
     if (n_jobs > 0) qk(0);
     if (n_jobs > 1) qk(1);
+    if (kAhead && n_jobs == 0) {                           // (no prefix)
+      ok = ok && wait_all(b.qfull + 8 * buf, qph[buf], abort_flag);     // (else a later unit's wait could meet this phase)
+      qph[buf] ^= 1;
+      if (lane == 0) mbar_arrive(b.qempty + 8 * buf);
+    }
     for (int i = 0; i < n_jobs && ok; ++i) {
       const int t = i & 1, k = i >> 1, step = two ? k : i;
       const int valid = step == x.steps - 1 ? last : kN;
@@ -246,6 +264,7 @@ __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, cons
       if (done && ++vs == L::NV) { vs = 0; vph ^= 1; }
       if (i + 2 < n_jobs) qk(i + 2);
     }
+    buf ^= 1;
   }
 }
 
@@ -300,16 +319,65 @@ __device__ __forceinline__ void fill_q(const AttnParams& p, const Row& r, uint32
   }
 }
 
-// A softmax warpgroup (tile t): turns S into P step by step and writes the result.  The Q rows of its next
-// unit are on their way while this one's result is written.
-template <int DH, bool kDirect>
+// The whole warp: brings the Q rows of every unit but the first (which the softmax warps, idle till then, fill in) into its
+// buffer, and asks for their own keys and values.
+template <int DH, bool kDirect, bool kOne>
+__device__ void load_q(const AttnParams& p, uint32_t smem, const Bars& b, int lane, volatile int* abort_flag) {
+  const int D = p.d.d_head, pieces = (D + 15) / 16 * 2, G = p.d.n_head / p.d.n_kv_head;     // 16-byte pieces, two per slice
+  const int per = 32 / pieces, own_c = lane % pieces, own_r = lane / pieces;
+  const int end = end_of(p);
+  uint32_t ph[2] = {1, 1};
+  int buf = 0;
+  for (int u = first_of(p); u < end;) {
+    const Unit x = unit_at(p, u, kUnitRows, kN);
+    const bool first = u == first_of(p);
+    u = after(p, u, x);
+    if (!wait_all(b.qempty + 8 * buf, ph[buf], abort_flag)) return;
+    ph[buf] ^= 1;
+    if (first) {
+      buf ^= 1;
+      continue;
+    }
+    const uint32_t tiles = smem + Smem<DH>::Q + buf * kQBuffer<DH, kOne>;
+    const int token0 = p.req[x.r].s0 * p.d.L_t;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)x.hk * G * D + own_c * 8;
+    if (own_r < per)                                       // (what a tile holds behind its rows reaches no result)
+      for (int r = own_r; r < x.rows; r += per) {
+        const int m = x.m0 + r, tok = fast_div(m, p.div_g);
+        const bool in = own_c * 8 < D;
+        const __nv_bfloat16* src = q + (in ? (token0 + tok) * p.d.q_token + (m - tok * G) * D : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(piece(tiles + (r >> 7) * Smem<DH>::TILE, r & 127, own_c)),
+                     "l"(src - (in ? 0 : own_c * 8)), "r"(in ? 16 : 0)
+                     : "memory");
+      }
+    if (kDirect && p.d.suffix_cap > 0)
+      for (int r = lane; r < x.rows; r += 32) {
+        const int tok = token0 + fast_div(x.m0 + r, p.div_g);
+        const int64_t at = (int64_t)fast_div(tok, p.div_lt) * p.d.suffix_seq + (int64_t)x.hk * p.d.suffix_head;
+        for (int i = 0; i < D; i += 64) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(p.k_suffix) + at + i));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(p.v_suffix) + at + i));
+        }
+      }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    mbar_arrive(b.qfull + 8 * buf);
+    buf ^= 1;
+  }
+}
+
+// A softmax warpgroup (tile t): turns S into P step by step and writes the result.  Where Q has one buffer,
+// its next rows are filled in here once the unit's products are done.
+template <int DH, bool kDirect, bool kOne>
 __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t smem, float* sml, const Bars& b,
                              volatile int* abort_flag) {
   using L = Smem<DH>;
   const AttnParams& p = tp.a;
   const int tid = threadIdx.x & 127, lane = tid & 31, wrow = tid & ~31;    // wrow: the warp's first row
   const uint32_t lanes = (uint32_t)wrow << 16;                              // its TMEM lanes
-  const uint32_t q_tile = smem + L::Q + t * L::TILE;
+  constexpr bool kAhead = kQAhead<DH, kOne>;
+  uint32_t q_tile = smem + L::Q + t * L::TILE, qph = 0;
+  int buf = 0;
   const uint32_t s_addr = tmem + t * kN + lanes, o_addr = tmem + 2 * kN + t * 128 + lanes;
   const int D = p.d.d_head;
   const float c = p.d.scale * kLog2e;
@@ -319,15 +387,20 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
   const int end = end_of(p);
   int u = first_of(p);
   Row next = row_at(p, u, t, tid);
-  fill_q<DH>(p, next, q_tile, tid);
+  if (!kOne || t == 0) fill_q<DH>(p, next, q_tile, tid);
   if (kDirect) ask_own(p, next);
+  if constexpr (kAhead) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane < 4) mbar_arrive(b.qfull);                    // 32 in all
+  }
   while (u < end && ok) {
-    const Row rw = next;
+    const Row rw = kAhead ? row_at(p, u, t, tid) : next;
     const Unit& x = rw.x;
     const RequestPlan& rq = p.req[x.r];
     const bool live = rw.live, warp_live = rw.warp_live;
     const int jobs = rw.jobs;
-    if (jobs > 0) {
+    if (!kAhead && jobs > 0) {
       fence_proxy_async_smem();
       mbar_arrive(b.qfull + 8 * t);
     }
@@ -428,6 +501,10 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
     float a = -INFINITY;
     const uint4* own_v = nullptr;
     if constexpr (kDirect) {
+      if constexpr (kAhead) {        // (every warp waits, also for rows it does not have: none gets units ahead)
+        q_tile = smem + L::Q + buf * kQBuffer<DH, kOne> + t * L::TILE;
+        if (!(ok = wait_all(b.qfull + 8 * buf, qph, abort_flag))) break;
+      }
       if (warp_live && (x.two || t == 0) && p.d.suffix_cap > 0) {
         const int seq = fast_div(rw.token, p.div_lt);
         own = live && visible_suffix(p, seq, rw.token - seq * p.d.L_t) > 0;
@@ -448,9 +525,15 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
           a = acc * c;
         }
       }
+      if constexpr (kAhead) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.qempty + 8 * buf);
+      }
     }
+    if (buf) qph ^= 1;
+    buf ^= 1;
     u = after(p, u, x);
-    const bool more = u < end;
+    const bool more = !kAhead && u < end;
     if (more) next = row_at(p, u, t, tid);
     // ---- the result of the unit's rows
     if (jobs > 0) {
@@ -558,7 +641,7 @@ __device__ void softmax_tile(const TcParams& tp, int t, uint32_t tmem, uint32_t 
   }
 }
 
-template <int DH, bool kDirect>
+template <int DH, bool kDirect, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ TcParams p) {
   using L = Smem<DH>;
   extern __shared__ uint8_t raw[];
@@ -570,16 +653,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   auto take = [&](int n) { const uint32_t r = at; at += 8 * n; return r; };
   b.kfull = take(L::NK); b.kempty = take(L::NK); b.vfull = take(L::NV); b.vempty = take(L::NV);
   b.qfull = take(2); b.sfull = take(2); b.pfull = take(4); b.odone = take(2);
-  b.ml_full = take(1); b.ml_empty = take(1);
+  b.ml_full = take(1); b.ml_empty = take(1); b.qempty = take(2);
+  constexpr bool kAhead = kQAhead<DH, kOne>;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::BAR + 248);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::BAR + 252);
-  static_assert((2 * L::NK + 2 * L::NV + 12) * 8 <= 248, "barriers");
+  static_assert((2 * L::NK + 2 * L::NV + 14) * 8 <= 248, "barriers");
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < L::NK; ++i) { mbar_init(b.kfull + 8 * i, 1); mbar_init(b.kempty + 8 * i, 1); }
     for (int i = 0; i < L::NV; ++i) { mbar_init(b.vfull + 8 * i, 1); mbar_init(b.vempty + 8 * i, 1); }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(b.qfull + 8 * t, 128);
+      mbar_init(b.qfull + 8 * t, kAhead ? 32 : 128);
+      mbar_init(b.qempty + 8 * t, kDirect ? 9 : 1);
       mbar_init(b.sfull + 8 * t, 1);
       mbar_init(b.pfull + 16 * t, 4);
       mbar_init(b.pfull + 16 * t + 8, 4);
@@ -602,11 +687,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
     if (warp == 8 && lane == 0) load_steps<DH>(p.a, &p.kmap, smem + L::K, L::NK, b.kfull, b.kempty, abort_flag);
     if (warp == 9 && lane == 0) load_steps<DH>(p.a, &p.vmap, smem + L::V, L::NV, b.vfull, b.vempty, abort_flag);
-    if (warp == 10) issue_mmas<DH>(p, tmem, smem, b, lane, abort_flag);
+    if (warp == 10) issue_mmas<DH, kOne>(p, tmem, smem, b, lane, abort_flag);
+    if (kAhead && warp == 11) load_q<DH, kDirect, kOne>(p.a, smem, b, lane, abort_flag);
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_tile<DH, kDirect>(p, warp >> 2, tmem, smem, reinterpret_cast<float*>(gbase + L::ML), b, abort_flag);
+    softmax_tile<DH, kDirect, kOne>(p, warp >> 2, tmem, smem, reinterpret_cast<float*>(gbase + L::ML), b, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -650,10 +736,10 @@ tr_status encode_map(CUtensorMap* map, const void* base, const AttnParams& p) {
   return TR_OK;
 }
 
-template <int DH, bool kDirect>
+template <int DH, bool kDirect, bool kOne>
 tr_status launch(const TcParams& p, int sms, cudaStream_t st) {
-  TR_TRY(ensure_smem_attr((const void*)prefix_kernel<DH, kDirect>, Smem<DH>::BYTES));
-  prefix_kernel<DH, kDirect><<<std::min(p.a.n_units, sms), kThreads, Smem<DH>::BYTES, st>>>(p);
+  TR_TRY(ensure_smem_attr((const void*)prefix_kernel<DH, kDirect, kOne>, Smem<DH>::BYTES));
+  prefix_kernel<DH, kDirect, kOne><<<std::min(p.a.n_units, sms), kThreads, Smem<DH>::BYTES, st>>>(p);
   TR_LAUNCH_CHECK("prefix_kernel");
   return TR_OK;
 }
@@ -668,8 +754,11 @@ tr_status launch_prefix_tc(const AttnParams& a, bool direct, cudaStream_t st) {
   TR_TRY(encode_map(&p.vmap, a.v_prefix, a));
   int sms = 0;
   TR_TRY(sm_count(&sms));
-  if (direct) return a.d.d_head <= 64 ? launch<64, true>(p, sms, st) : launch<128, true>(p, sms, st);
-  return a.d.d_head <= 64 ? launch<64, false>(p, sms, st) : launch<128, false>(p, sms, st);
+  if (a.d.d_head <= 64) return direct ? launch<64, true, false>(p, sms, st) : launch<64, false, false>(p, sms, st);
+  bool one = true;
+  for (int r = 0; r < a.R; ++r) one = one && request_rows(a, r) / a.d.n_kv_head <= kM;
+  if (one) return direct ? launch<128, true, true>(p, sms, st) : launch<128, false, true>(p, sms, st);
+  return direct ? launch<128, true, false>(p, sms, st) : launch<128, false, false>(p, sms, st);
 }
 
 }  // namespace attn
