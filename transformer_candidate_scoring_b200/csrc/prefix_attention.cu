@@ -391,11 +391,16 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
   const RequestPlan& rq = p.req[request_of(p, s)];
   const int64_t rows = (int64_t)(rq.s1 - rq.s0) * p.d.L_t * H;
   const int chunks = D / 8, first = warp / parts * parts, n_results = results_of(p, rq);
-  for (int item = part * 32 + lane; item < min(8, n_rows - row0) * chunks; item += parts * 32) {
+  const int items = min(8, n_rows - row0) * chunks;
+  // `share` neighbouring lanes divide a row's results where threads are to spare
+  int share = 1;
+  while (share < 8 && 4 * share < n_results && items * share * 2 <= parts * 32) share *= 2;
+  for (int at = part * 32 + lane; at < items * share; at += parts * 32) {
+    const int item = at / share, mine = at % share;
     const int rr = item / chunks, c0 = item % chunks * 8, r = row0 + rr;
     const int64_t row = ((int64_t)s * p.d.L_t + r / G) * H + hk * G + r % G;
     Running x;
-    for (int i = 0; i < parts; ++i) {
+    for (int i = mine; i < parts; i += share) {
       const float mm = s_m[first + i][rr];
       float base;
       x.rescale(fmaxf(x.m, mm), &base);
@@ -406,7 +411,16 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x.o[e] = fmaf(f, w[e], x.o[e]);
     }
-    merge_prefix(p, n_results, rq.part + (row - (int64_t)rq.s0 * p.d.L_t * H), rows, c0, true, 0, 1, x);
+    merge_prefix(p, n_results, rq.part + (row - (int64_t)rq.s0 * p.d.L_t * H), rows, c0, true, mine, share, x);
+    for (int y = 1; y < share; y <<= 1) {
+      const uint32_t group = ((1u << share) - 1) << (lane & ~(share - 1));
+      float base;                                          // (both lanes': then their sums add up)
+      x.rescale(fmaxf(x.m, __shfl_xor_sync(group, x.m, y)), &base);
+      x.l += __shfl_xor_sync(group, x.l, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.o[e] += __shfl_xor_sync(group, x.o[e], y);
+    }
+    if (mine > 0) continue;
     store_row<__nv_bfloat16>(p, row, c0, x);
     if (p.lse && c0 == 0) p.lse[row] = x.lse();
   }
@@ -414,8 +428,10 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
 
 template <int kBlocks, bool kCausal>
 tr_status launch_suffix(const AttnParams& p, cudaStream_t st) {
-  // a warp per 16 keys up to the four of a CTA
-  const int steps = (p.d.suffix_cap + 15) / 16, parts = steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
+  // a warp per 16 keys or per eight results of the prefix, up to the four of a CTA
+  int steps = (p.d.suffix_cap + 15) / 16;
+  for (int r = 0; r < p.R; ++r) steps = std::max(steps, p.req[r].n_split / 8);
+  const int parts = steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
   const int r_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 7) / 8, units = kSuffixThreads / 32 / parts;
   const int64_t n_unit = (int64_t)p.req[p.R].s0 * p.d.n_kv_head * r_tiles;
   return launch_dependent(p.n_units > 0, suffix_kernel<kBlocks, kCausal>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
@@ -453,11 +469,11 @@ tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t
 }
 
 // How many steps of keys a unit takes.  Fewer steps give more units to spread over the `slots` (SMs,
-// or CTAs that share one), but every unit costs about three tile steps (Q, the first scores, the
-// result) and every chunk of a prefix a partial result per row.  The candidates are: no split, and
+// or CTAs that share one), but every unit costs about three more (kUnitSteps) and every chunk of a prefix a partial result per row.  The candidates are: no split, and
 // the shortest chunks that give one, two or four units per slot.  With `direct`, no split also saves the
 // merge's launch (about 4 us), and requests without a prefix have one (empty) unit per 256 rows.
-// With `runs`, equal runs of steps are a candidate too, at a unit more per CTA.
+// With `runs`, equal runs of steps are a candidate too, at a unit more per CTA: 16 requests of 2048 to 8192 tokens
+// and 32 sequences take 107 us by runs and 122 without, the 18 requests at kUnitSteps 45 and 50.
 void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool direct, bool runs) {
   const int G = p.d.n_head / p.d.n_kv_head;
   int steps[TR_MAX_REQUESTS], n_m[TR_MAX_REQUESTS];
@@ -493,18 +509,21 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool dir
     const double waves = (double)((units(c) + slots - 1) / slots);
     const double split = (double)ceil_div(longest, c);
     const double bytes = split > 1 ? (double)rows_all * split * p.d.d_head * 8.0 : 0.0;
-    const double cost = waves * (c * (two ? 2.0 : 1.0) + 3.0) + bytes / 3.5e6 + (direct && split > 1 ? 6.0 : 0.0);
+    const double cost = waves * (c * (two ? 2.0 : 1.0) + kUnitSteps) + bytes / 3.5e6 + (direct && split > 1 ? 6.0 : 0.0);
     if (cost < best_cost) {
       best_cost = cost;
       best = c;
     }
   }
   if (runs && longest > 0 && p.d.n_kv_head <= slots && *std::max_element(n_m, n_m + p.R) == 1) {
-    int line = 0, filled = 0;                 // (below 2^24 + R steps)
-    for (int r = 0; r < p.R; ++r) line += steps[r], filled += steps[r] > 0;
+    int line = 0, filled = 0;                 // (below 2^24 + R (1 + kUnitSteps))
+    for (int r = 0; r < p.R; ++r) {
+      line += steps[r] > 0 ? steps[r] + kUnitSteps : 0;
+      filled += steps[r] > 0;
+    }
     const int run = ceil_div(line, slots / p.d.n_kv_head), n = ceil_div(line, run);
     const double split = 1.0 + (double)line / ((double)run * filled);
-    const double cost = run * (two ? 2.0 : 1.0) + 3.0 * (n + filled) / n + (double)rows_all * split * p.d.d_head * 8.0 / 3.5e6 +
+    const double cost = run * (two ? 2.0 : 1.0) + kUnitSteps + (double)rows_all * split * p.d.d_head * 8.0 / 3.5e6 +
                         (direct ? 6.0 : 0.0);
     if (cost < best_cost) {
       p.run = run;
@@ -518,14 +537,15 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool dir
     RequestPlan& q = p.req[r];
     q.first_unit = unit;
     q.chunk = p.run > 0 ? steps[r] : best;
-    // (a line of n steps meets at most ceil(n / run) + 1 runs)
-    q.n_split = p.run > 0 ? (steps[r] > 0 ? ceil_div(steps[r], p.run) + 1 : 0) : ceil_div(steps[r], best);
+    // (n places meet at most ceil(n / run) + 1 runs)
+    const int places = steps[r] > 0 ? steps[r] + kUnitSteps : 0;
+    q.n_split = p.run > 0 ? (places > 0 ? ceil_div(places, p.run) + 1 : 0) : ceil_div(steps[r], best);
     if (direct && p.run == 0 && best >= longest && q.s1 > q.s0) q.n_split = 1;
     q.n_m = n_m[r];
     q.div_m = fast_div_by((uint32_t)std::max(q.n_m, 1));
     q.div_split = fast_div_by((uint32_t)std::max(q.n_split, 1));
     q.part = part;
-    unit += p.run > 0 ? steps[r] : p.d.n_kv_head * n_m[r] * q.n_split;
+    unit += p.run > 0 ? places : p.d.n_kv_head * n_m[r] * q.n_split;
     part += request_rows(p, r) * q.n_split;
   }
   p.req[p.R].first_unit = unit;

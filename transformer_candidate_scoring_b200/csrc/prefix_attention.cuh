@@ -14,15 +14,18 @@ constexpr int kMaxDHead = 128;
 // of the fp32 one, whose units are 64 rows, or 16 where no key head has more than 32.
 constexpr int kUnitRows = 256, kStepKeys = 128;
 constexpr int kStepKeysF32 = 64;
+// What a unit costs beside its keys (Q, the first scores, the result), in steps.  (18 requests of 0 to 5990
+// tokens, 4 sequences each, 32 heads of 128 on 8: with 3, 5 and 8 steps 47, 45 and 46 us.)
+constexpr int kUnitSteps = 5;
 
 // The prefix part of one request: rows = sequences x query tokens x heads of a key head.  A unit
 // is up to `unit_rows` of them of one key head over `chunk` steps of keys; a prefix of several chunks
 // gives each row several partial results.
 //
 // Where no key head has more rows than a unit (each key is read by one CTA), the cut may be by runs
-// instead (`run` > 0): the steps of all requests stand in one line, of which a team of n_kv_head CTAs, one
-// per key head, takes `run`; a unit is what of a run belongs to one request.  However the prefixes' lengths
-// differ, every CTA has the same share, and a token's key heads, neighbours in memory, are read together.
+// instead (`run` > 0): the steps of all requests stand in one line, each request's behind kUnitSteps places
+// without keys, and a team of n_kv_head CTAs, one per key head, takes `run` places of it; a unit is what of a
+// run belongs to one request.  However the prefixes' lengths differ, every CTA has the same share.
 
 // n / d for 0 <= n < 2^31 as a multiplication: (mulhi(n, mul) + n) >> shift, after Granlund and Montgomery,
 // "Division by Invariant Integers using Multiplication".
@@ -40,7 +43,7 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
 }
 
 struct RequestPlan {
-  int first_unit;      // units (with runs: steps) of request r: first_unit[r] .. first_unit[r+1]-1
+  int first_unit;      // units (with runs: places) of request r: first_unit[r] .. first_unit[r+1]-1
   int n_split;         // partial results per row, with runs at most (0: no prefix or no sequences)
   int chunk;           // steps per chunk; with runs, of the prefix
   int p0, p1;          // prefix tokens
@@ -75,7 +78,7 @@ __host__ __device__ inline int64_t request_rows(const AttnParams& p, int r) {
 // Partial results of a row of request q.
 __device__ __forceinline__ int results_of(const AttnParams& p, const RequestPlan& q) {
   if (p.run == 0 || q.n_split == 0) return q.n_split;
-  return fast_div(q.first_unit + q.chunk - 1, p.div_run) - fast_div(q.first_unit, p.div_run) + 1;
+  return fast_div(q.first_unit + kUnitSteps + q.chunk - 1, p.div_run) - fast_div(q.first_unit, p.div_run) + 1;
 }
 
 struct Unit {
@@ -103,8 +106,9 @@ __device__ __forceinline__ Unit unit_at(const AttnParams& p, int u, int unit_row
     x.hk = blockIdx.x - team * p.d.n_kv_head;
     x.m0 = 0;
     x.split = team - fast_div(q.first_unit, p.div_run);
-    x.tok = q.p0 + i * step_keys;
-    x.steps = min(q.chunk - i, (team + 1) * p.run - u);
+    const int step = max(i - kUnitSteps, 0);
+    x.tok = q.p0 + step * step_keys;
+    x.steps = max(min(q.chunk, (team + 1) * p.run - q.first_unit - kUnitSteps) - step, 0);
   } else {
     const int im = fast_div(i, q.div_m);
     x.m0 = (i - im * q.n_m) * unit_rows;      // units that share keys are neighbours
@@ -115,7 +119,7 @@ __device__ __forceinline__ Unit unit_at(const AttnParams& p, int u, int unit_row
   }
   x.rows = min(unit_rows, m_all - x.m0);
   x.two = x.rows > unit_rows / 2;
-  x.keys = min(x.steps * step_keys, q.p1 - x.tok);
+  x.keys = min(x.steps * step_keys, q.p1 - x.tok);         // (none where a run ends before a request's first key)
   x.steps = (x.keys + step_keys - 1) / step_keys;
   return x;
 }
@@ -125,7 +129,11 @@ __device__ __forceinline__ int first_of(const AttnParams& p) { return p.run > 0 
 __device__ __forceinline__ int end_of(const AttnParams& p) {
   return p.run > 0 ? min((fast_div(blockIdx.x, p.div_kv) + 1) * p.run, p.req[p.R].first_unit) : p.n_units;
 }
-__device__ __forceinline__ int after(const AttnParams& p, int u, const Unit& x) { return p.run > 0 ? u + x.steps : u + gridDim.x; }
+__device__ __forceinline__ int after(const AttnParams& p, int u, const Unit& x) {
+  if (p.run == 0) return u + gridDim.x;
+  const RequestPlan& q = p.req[x.r];          // the request's end or the run's, whichever is first
+  return min(q.first_unit + kUnitSteps + q.chunk, (x.split + fast_div(q.first_unit, p.div_run) + 1) * p.run);
+}
 
 // Suffix keys that query token t of sequence s sees; a length outside the buffer is clamped.
 __device__ __forceinline__ int visible_suffix(const AttnParams& p, int64_t s, int t) {
