@@ -250,13 +250,13 @@ def topk(scores: torch.Tensor, req_offsets: Sequence[int], k: int, out_idx: torc
 
 def _on(*tensors) -> int:
     """The device ordinal that all of ``tensors`` (None aside) are on."""
-    dev = -1
+    dev = -2
     for t in tensors:
         if t is not None:
             d = t.get_device()
-            if d < 0:
-                raise ValueError("expected CUDA tensors")
             if d != dev:
+                if d < 0:
+                    raise ValueError("expected CUDA tensors")
                 if dev >= 0:
                     raise ValueError(f"tensors on different devices: cuda:{dev} and cuda:{d}")
                 dev = d
@@ -269,27 +269,29 @@ def _run(dev: int, stream, call, *args) -> None:
         raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == dev:
-        _check(call(*args, raw))
+    if torch._C._cuda_getDevice() == dev:
+        status = call(*args, raw)
+        if status:
+            _check(status)
     else:
         with torch.cuda.device(dev):
             _check(call(*args, raw))
 
 
-def _new(shape, dtype, dev: int, stream) -> torch.Tensor:
-    """A buffer from torch's allocator for work on ``stream`` (None: the current one), kept from
-    reuse until that work is done."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A buffer on the device of ``like`` from torch's allocator for work on ``stream`` (None: the current
+    one), kept from reuse until that work is done."""
+    t = like.new_empty(shape, dtype=dtype)
     if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev))
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.get_device()))
     return t
 
 
-def _workspace(workspace, need: int, dev: int, stream):
-    """``workspace`` if it is large enough, or a new buffer of ``need`` bytes; and its size."""
+def _workspace(workspace, need: int, like: torch.Tensor, stream):
+    """``workspace`` if it is large enough, or a new buffer of ``need`` bytes on the device of ``like``; and its size."""
     if workspace is None:
-        return _new((max(need, 16),), torch.uint8, dev, stream), need
-    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        return _new(like, (max(need, 16),), torch.uint8, stream), need
+    if not workspace.is_contiguous() or workspace.get_device() != like.get_device():
         raise ValueError("workspace: expected a contiguous tensor on the inputs' device")
     size = workspace.numel() * workspace.element_size()
     if size < need:
@@ -375,17 +377,21 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
         _layout(q), _layout(k_prefix), _layout(v_prefix), _layout(k_suffix), _layout(v_suffix), _layout(suffix_len),
         tuple(map(int, prefix_offsets)), tuple(map(int, seq_offsets)), None if scale is None else float(scale), bool(causal), dev)
     if out is None:
-        out = _new(q.shape, q.dtype, dev, stream)
+        out = torch.empty_like(q) if stream is None and q.is_contiguous() else _new(q, q.shape, q.dtype, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out: expected q's shape and type")
+    else:
+        _ptr(out)
     if lse is None:
-        lse = _new(q.shape[:-1], torch.float32, dev, stream)
+        lse = _new(q, q.shape[:-1], torch.float32, stream)
     elif lse.shape != q.shape[:-1] or lse.dtype != torch.float32:
         raise ValueError("lse: expected fp32 of q's shape without the last dimension")
-    ws, size = _workspace(workspace, need, dev, stream) if need else (None, 0)
+    else:
+        _ptr(lse)
+    ws, size = _workspace(workspace, need, q, stream) if need else (None, 0)
     _run(dev, stream, L.load().tr_prefix_attention, desc, q.data_ptr(), so, k_prefix.data_ptr(), v_prefix.data_ptr(), po,
          k_suffix.data_ptr() if S else None, v_suffix.data_ptr() if S else None, suffix_len.data_ptr() if S else None, R,
-         _ptr(out), _ptr(lse), ws.data_ptr() if need else None, size)
+         out.data_ptr(), lse.data_ptr(), ws.data_ptr() if need else None, size)
     return out, lse
 
 
@@ -429,18 +435,20 @@ def beam_select(logits: torch.Tensor, cum: torch.Tensor, k: int, *, finished: to
     k = int(k)
     code, ld, allowed_ld, R, W, V, need = _select_plan(_layout(logits), _layout(cum), _layout(finished), _layout(allowed), k)
     for name, t, dt in (("parent", parent, torch.int32), ("token", token, torch.int32), ("score", score, torch.float32)):
-        if t is not None and (t.shape != (R, k) or t.dtype != dt):
-            raise ValueError(f"{name}: expected {dt} [R, k]")
+        if t is not None:
+            if t.shape != (R, k) or t.dtype != dt:
+                raise ValueError(f"{name}: expected {dt} [R, k]")
+            _ptr(t)
     if parent is None:
-        parent = _new((R, k), torch.int32, dev, stream)
+        parent = _new(logits, (R, k), torch.int32, stream)
     if token is None:
-        token = _new((R, k), torch.int32, dev, stream)
+        token = _new(logits, (R, k), torch.int32, stream)
     if score is None:
-        score = _new((R, k), torch.float32, dev, stream)
-    ws, size = _workspace(workspace, need, dev, stream)
+        score = _new(logits, (R, k), torch.float32, stream)
+    ws, size = _workspace(workspace, need, logits, stream)
     _run(dev, stream, L.load().tr_beam_select, logits.data_ptr(), code, ld, _ptr(cum), _ptr(finished),
-         None if allowed is None else allowed.data_ptr(), allowed_ld, R, W, V, k, int(pad_token), _ptr(parent), _ptr(token),
-         _ptr(score), ws.data_ptr(), size)
+         None if allowed is None else allowed.data_ptr(), allowed_ld, R, W, V, k, int(pad_token), parent.data_ptr(), token.data_ptr(),
+         score.data_ptr(), ws.data_ptr(), size)
     return parent, token, score
 
 
@@ -474,24 +482,24 @@ def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor, outs: Seq
     if not states or not R:
         return dsts
     W_in = states[0].shape[0] // R
-    flat = []
+    flat, last = [], None
     for i, (s, o) in enumerate(zip(states, dsts)):
-        size = s.element_size()
-        rows, stride, row_bytes = _row_layout(s.shape, s.stride(), size)
-        if o is s:
-            o_rows, o_stride, o_bytes = rows, stride, row_bytes
-        else:
-            o_rows, o_stride, o_bytes = _row_layout(o.shape, o.stride(), size)
+        layout = (s.shape, s.stride(), s.dtype, o.shape, o.stride(), o.dtype)
+        if layout != last:                # (the states of a decoder's layers are alike)
+            size = s.element_size()
+            rows, stride, row_bytes = _row_layout(layout[0], layout[1], size)
+            o_rows, o_stride, _ = _row_layout(layout[3], layout[4], size)
             if o.dtype != s.dtype or o.shape[1:] != s.shape[1:]:
                 raise ValueError(f"state {i}: its out differs in row shape or type")
-        if rows != R * W_in or o_rows != R * W_out:
-            raise ValueError(f"state {i}: expected rows [R*W_in, ...] and an out [R*W_out, ...]")
+            if rows != R * W_in or o_rows != R * W_out:
+                raise ValueError(f"state {i}: expected rows [R*W_in, ...] and an out [R*W_out, ...]")
+            last = layout
         flat += (o.data_ptr(), s.data_ptr(), o_stride, stride, row_bytes)
     call, par = L.load().tr_beam_reorder, _ptr(parent)
     for i in range(0, len(states), L.TR_MAX_STATES):
         m = min(L.TR_MAX_STATES, len(states) - i)
         packed = struct.pack("=" + "QQqqq" * m, *flat[5 * i:5 * (i + m)])
-        _run(dev, stream, call, C.cast(packed, C.POINTER(L.BeamState)), m, par, R, W_in, W_out)
+        _run(dev, stream, call, packed, m, par, R, W_in, W_out)
     return dsts
 
 
