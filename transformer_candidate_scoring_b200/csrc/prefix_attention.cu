@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   const int64_t row = live ? row_at : p.n_rows - 1;
   const int D = p.d.d_head, H = p.d.n_head, c0 = tl * 8;
   const bool in = c0 < D;
-  const int h = (int)(row % H);
-  const int64_t st = row / H, s = st / p.d.L_t;
-  const int t = (int)(st % p.d.L_t), hk = h / (H / p.d.n_kv_head);
+  const int tk = fast_div((int)row, p.div_h), h = (int)row - tk * H;       // (rows are below 2^31)
+  const int64_t st = tk, s = fast_div(tk, p.div_lt);
+  const int t = tk - (int)s * p.d.L_t, hk = fast_div(h, p.div_g);
   const RequestPlan& rq = p.req[request_of(p, s)];
   const float c = p.d.scale * kLog2e;
   Running x;
@@ -253,24 +253,25 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
 
 template <int kBlocks, bool kCausal>     // 64-wide blocks of d_head
 __global__ void __launch_bounds__(kSuffixThreads, kBlocks == 1 ? 6 : 4)
-suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
+suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, const FastDiv div_tiles, const FastDiv div_chunks) {
   constexpr int DP = kBlocks * 64;
   __shared__ float s_o[kSuffixThreads / 32][8][DP + 4], s_m[kSuffixThreads / 32][8], s_l[kSuffixThreads / 32][8];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4;
-  const int units = kSuffixThreads / 32 / parts, part = warp % parts, D = p.d.d_head, H = p.d.n_head, Hk = p.d.n_kv_head;
-  const int G = H / Hk, n_rows = p.d.L_t * G;
+  const int parts = 1 << log_parts, part = warp & (parts - 1), D = p.d.d_head, H = p.d.n_head, Hk = p.d.n_kv_head;
+  const int G = p.group, n_rows = p.d.L_t * G;
   const int n_unit = p.req[p.R].s0 * Hk * r_tiles;         // below 2^31: no more than query rows
-  const int u_at = blockIdx.x * units + warp / parts, u = min(u_at, n_unit - 1);
-  const int s = u / (Hk * r_tiles), hk = u / r_tiles % Hk, row0 = u % r_tiles * 8;   // rows t * G + head in group
+  const int u_at = ((int)blockIdx.x * (kSuffixThreads / 32) + warp) >> log_parts, u = min(u_at, n_unit - 1);
+  const int sh = fast_div(u, div_tiles), s = fast_div(sh, p.div_kv), hk = sh - s * Hk;
+  const int row0 = (u - sh * r_tiles) * 8;                 // rows t * G + head in group
   const float c = p.d.scale * kLog2e;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int len = visible_suffix(p, s, p.d.L_t - 1);       // what the last query token sees: all of it
   // ---- Q: 16 bytes of row g per 32 columns
   uint4 q[2 * kBlocks];
   {
-    const int r = row0 + g;
+    const int r = row0 + g, t = fast_div(r, p.div_g);
     const __nv_bfloat16* src =
-        static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)s * p.d.L_t + r / G) * p.d.q_token + (hk * G + r % G) * D;
+        static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)s * p.d.L_t + t) * p.d.q_token + (hk * G + r - t * G) * D;
 #pragma unroll
     for (int i = 0; i < 2 * kBlocks; ++i)
       q[i] = r < n_rows && i * 32 + qd * 8 < D ? __ldg(reinterpret_cast<const uint4*>(src + i * 32 + qd * 8)) : zero;
@@ -279,8 +280,8 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
   int seen[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
-    seen[e] = kCausal ? max(0, len - max(0, p.d.L_t - 1 - (row0 + 2 * qd + e) / G)) : len;
-  const int seen_by_all = kCausal ? max(0, len - (p.d.L_t - 1 - row0 / G)) : len;
+    seen[e] = kCausal ? max(0, len - max(0, p.d.L_t - 1 - fast_div(row0 + 2 * qd + e, p.div_g))) : len;
+  const int seen_by_all = kCausal ? max(0, len - (p.d.L_t - 1 - fast_div(row0, p.div_g))) : len;
   const int64_t so = (int64_t)s * p.d.suffix_seq + hk * p.d.suffix_head;
   const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(p.k_suffix) + so, *vp = static_cast<const __nv_bfloat16*>(p.v_suffix) + so;
   float o[4 * kBlocks][4] = {};                            // O^T: 16 columns of d_head x 8 rows
@@ -390,15 +391,15 @@ suffix_kernel(const __grid_constant__ AttnParams p, int parts, int r_tiles) {
   if (u_at >= n_unit) return;
   const RequestPlan& rq = p.req[request_of(p, s)];
   const int64_t rows = (int64_t)(rq.s1 - rq.s0) * p.d.L_t * H;
-  const int chunks = D / 8, first = warp / parts * parts, n_results = results_of(p, rq);
+  const int chunks = D / 8, first = warp - part, n_results = results_of(p, rq);
   const int items = min(8, n_rows - row0) * chunks;
   // `share` neighbouring lanes divide a row's results where threads are to spare
-  int share = 1;
-  while (share < 8 && 4 * share < n_results && items * share * 2 <= parts * 32) share *= 2;
+  int share = 1, log_share = 0;
+  while (share < 8 && 4 * share < n_results && items * share * 2 <= parts * 32) share = 1 << ++log_share;
   for (int at = part * 32 + lane; at < items * share; at += parts * 32) {
-    const int item = at / share, mine = at % share;
-    const int rr = item / chunks, c0 = item % chunks * 8, r = row0 + rr;
-    const int64_t row = ((int64_t)s * p.d.L_t + r / G) * H + hk * G + r % G;
+    const int item = at >> log_share, mine = at & (share - 1);
+    const int rr = fast_div(item, div_chunks), c0 = (item - rr * chunks) * 8, r = row0 + rr, t = fast_div(r, p.div_g);
+    const int64_t row = ((int64_t)s * p.d.L_t + t) * H + hk * G + r - t * G;
     Running x;
     for (int i = mine; i < parts; i += share) {
       const float mm = s_m[first + i][rr];
@@ -431,11 +432,11 @@ tr_status launch_suffix(const AttnParams& p, cudaStream_t st) {
   // a warp per 16 keys or per eight results of the prefix, up to the four of a CTA
   int steps = (p.d.suffix_cap + 15) / 16;
   for (int r = 0; r < p.R; ++r) steps = std::max(steps, p.req[r].n_split / 8);
-  const int parts = steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
-  const int r_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 7) / 8, units = kSuffixThreads / 32 / parts;
+  const int log_parts = steps >= 4 ? 2 : steps >= 2 ? 1 : 0;
+  const int r_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 7) / 8, units = (kSuffixThreads / 32) >> log_parts;
   const int64_t n_unit = (int64_t)p.req[p.R].s0 * p.d.n_kv_head * r_tiles;
   return launch_dependent(p.n_units > 0, suffix_kernel<kBlocks, kCausal>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
-                          parts, r_tiles);
+                          log_parts, r_tiles, fast_div_by((uint32_t)r_tiles), fast_div_by((uint32_t)(p.d.d_head / 8)));
 }
 
 tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t* prefix, int R) {
@@ -566,6 +567,8 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
   p.div_g = fast_div_by((uint32_t)(d->n_head / d->n_kv_head));
   p.div_lt = fast_div_by((uint32_t)d->L_t);
   p.div_kv = fast_div_by((uint32_t)d->n_kv_head);
+  p.div_h = fast_div_by((uint32_t)d->n_head);
+  p.group = d->n_head / d->n_kv_head;
   for (int r = 0; r <= R; ++r) {
     RequestPlan& q = p.req[r];
     q.s0 = (int)seq[r];

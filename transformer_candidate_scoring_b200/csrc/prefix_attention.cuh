@@ -64,7 +64,8 @@ struct AttnParams {
   int run;             // steps per CTA, 0: units of `chunk` steps
   int64_t n_rows;      // query rows of all requests: n * L_t * n_head
   FastDiv div_g, div_lt;   // by n_head / n_kv_head, by L_t
-  FastDiv div_run, div_kv; // by run, by n_kv_head
+  FastDiv div_run, div_kv, div_h;   // by run, n_kv_head, n_head
+  int group;           // n_head / n_kv_head
   // partial result i of row `row` of request r (its rows counted from 0, head fastest) is
   // part_o[(part + i * rows of r + row) * d_head ..] and part_lse[the same] (times log2 e)
   float *part_o, *part_lse;
@@ -97,7 +98,7 @@ __device__ __forceinline__ Unit unit_at(const AttnParams& p, int u, int unit_row
     if (p.req[mid].first_unit <= u) lo = mid; else hi = mid - 1;
   }
   const RequestPlan& q = p.req[lo];
-  const int m_all = (q.s1 - q.s0) * p.d.L_t * (p.d.n_head / p.d.n_kv_head);
+  const int m_all = (q.s1 - q.s0) * p.d.L_t * p.group;
   const int i = u - q.first_unit;
   Unit x;
   x.r = lo;

@@ -282,7 +282,7 @@ __device__ __forceinline__ Row row_at(const AttnParams& p, int u, int t, int tid
   r.jobs = r.x.jobs(t);
   r.live = r.base + tid < r.x.rows;
   r.warp_live = r.base + (tid & ~31) < r.x.rows;
-  const int G = p.d.n_head / p.d.n_kv_head, m = r.x.m0 + r.base + tid;     // row within (request, key head)
+  const int G = p.group, m = r.x.m0 + r.base + tid;     // row within (request, key head)
   const int tok = fast_div(m, p.div_g);
   r.token = p.req[r.x.r].s0 * p.d.L_t + tok;
   r.head = r.x.hk * G + m - tok * G;
@@ -323,7 +323,7 @@ __device__ __forceinline__ void fill_q(const AttnParams& p, const Row& r, uint32
 // buffer, and asks for their own keys and values.
 template <int DH, bool kDirect, bool kOne>
 __device__ void load_q(const AttnParams& p, uint32_t smem, const Bars& b, int lane, volatile int* abort_flag) {
-  const int D = p.d.d_head, pieces = (D + 15) / 16 * 2, G = p.d.n_head / p.d.n_kv_head;     // 16-byte pieces, two per slice
+  const int D = p.d.d_head, pieces = (D + 15) / 16 * 2, G = p.group;     // 16-byte pieces, two per slice
   const int per = 32 / pieces, own_c = lane % pieces, own_r = lane / pieces;
   const int end = end_of(p);
   uint32_t ph[2] = {1, 1};
