@@ -210,6 +210,20 @@ def test_attention_causal_rows_ignore_later_values(api, dtype, bad, d):
     assert torch.equal(got[1], clean[1])                    # scores do not read values
 
 
+# More units of rows than SMs, the last wave of them less than half full, the last unit of a key head shorter than a tile.
+WAVES = [([2400], [130], 16, 16, 16, 1, 1, False), ([2300, 7], [129, 0], 20, 20, 128, 0, 1, False),
+         ([2400], [70], 16, 16, 104, 2, 1, False), ([1203], [300], 16, 16, 64, 4, 2, True)]
+
+
+@pytest.mark.parametrize("case", WAVES, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}x{c[4]}-s{c[5]}".replace(" ", ""))
+def test_attention_partial_last_wave(api, case):
+    counts, prefix, H, H_kv, d, S, L_t, causal = case
+    x = attn_inputs(18, counts, prefix, H, H_kv, d, S, L_t)
+    got = call(api, dev(x), causal=causal)
+    ok(api)
+    agrees(got, x, d ** -0.5, causal)
+
+
 RAGGED = [5003, 1, 700, 2049, 4100, 128, 127, 5990, 3333, 129, 64, 2500, 1111, 5500, 900, 0, 4999, 2222]
 RUNS = [
     # counts, prefix, H, H_kv, d, S, L_t, causal

@@ -42,6 +42,8 @@ __device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
   return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift);
 }
 
+constexpr int kNoHalves = 0x7FFFFFFF;
+
 struct RequestPlan {
   int first_unit;      // units (with runs: places) of request r: first_unit[r] .. first_unit[r+1]-1
   int n_split;         // partial results per row, with runs at most (0: no prefix or no sequences)
@@ -61,6 +63,7 @@ struct AttnParams {
   int* status;
   tr_attn_desc d;
   int R, n_units;      // (with runs, the CTAs)
+  int halves;          // from this unit on, each is two of half the rows (kNoHalves: none)
   int run;             // steps per CTA, 0: units of `chunk` steps
   int64_t n_rows;      // query rows of all requests: n * L_t * n_head
   FastDiv div_g, div_lt;   // by n_head / n_kv_head, by L_t
@@ -92,6 +95,13 @@ struct Unit {
 };
 
 __device__ __forceinline__ Unit unit_at(const AttnParams& p, int u, int unit_rows, int step_keys) {
+  const bool halved = u >= p.halves;
+  int half = 0;
+  if (halved) {
+    half = (u - p.halves) & 1;
+    u = p.halves + ((u - p.halves) >> 1);
+    unit_rows /= 2;
+  }
   int lo = 0, hi = p.R - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -112,14 +122,14 @@ __device__ __forceinline__ Unit unit_at(const AttnParams& p, int u, int unit_row
     x.steps = max(min(q.chunk, (team + 1) * p.run - q.first_unit - kUnitSteps) - step, 0);
   } else {
     const int im = fast_div(i, q.div_m);
-    x.m0 = (i - im * q.n_m) * unit_rows;      // units that share keys are neighbours
+    x.m0 = (i - im * q.n_m) * (unit_rows << halved) + half * unit_rows;      // units that share keys are neighbours
     x.hk = fast_div(im, q.div_split);
     x.split = im - x.hk * q.n_split;
     x.tok = q.p0 + x.split * q.chunk * step_keys;
     x.steps = q.chunk;
   }
   x.rows = min(unit_rows, m_all - x.m0);
-  x.two = x.rows > unit_rows / 2;
+  x.two = !halved && x.rows > unit_rows / 2;
   x.keys = min(x.steps * step_keys, q.p1 - x.tok);         // (none where a run ends before a request's first key)
   x.steps = (x.keys + step_keys - 1) / step_keys;
   return x;
