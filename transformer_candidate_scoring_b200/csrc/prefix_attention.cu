@@ -552,10 +552,10 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool dir
   p.req[p.R].first_unit = unit;
   p.halves = kNoHalves;
   if (p.run == 0) p.n_units = unit;
-  // A last wave that leaves half of the SMs idle: its units in halves, one tile of rows each, take half the
+  // A last or only wave that leaves half of the SMs idle: its units in halves, one tile of rows each, take half the
   // time (2 requests x 4096 sequences over 4096 tokens, 16 heads of 128 on 4, 3.46 waves: 315 -> 286 us)
   const int rest = unit % slots;
-  if (runs && p.run == 0 && two && unit > slots && rest > 0 && 2 * rest <= slots) {
+  if (runs && p.run == 0 && two && rest > 0 && 2 * rest <= slots) {
     p.halves = unit - rest;
     p.n_units = unit + rest;
   }
