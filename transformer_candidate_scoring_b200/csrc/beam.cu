@@ -321,7 +321,7 @@ __device__ __forceinline__ uint32_t bisect_by(const uint32_t* keys, int want, ui
   return a;
 }
 // Over the first `count` of at most 1024 keys (those behind them, up to the next power of two, are 0).
-__device__ __forceinline__ uint32_t bisect(const uint32_t* keys, int count, int want, uint32_t floor) {
+__device__ __noinline__ uint32_t bisect(const uint32_t* keys, int count, int want, uint32_t floor) {
   return count <= 128 ? bisect_by<4>(keys, want, floor) : count <= 512 ? bisect_by<16>(keys, want, floor) : bisect_by<32>(keys, want, floor);
 }
 

@@ -41,7 +41,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <int RT, int DP>     // rows per thread (8 threads down), d_head padded to 64 or 128
+template <int RT, int DP>     // rows per thread (8 threads down), d_head padded to 64, 96 or 128
 struct Layout {
   static constexpr int BM = 8 * RT, KP = DP + 4;
   static constexpr int Q = 0, K = Q + BM * DP, V = K + kN * KP, P = V + kN * DP;
@@ -65,7 +65,8 @@ __device__ __forceinline__ void copy_keys(float* dst, int pitch, const float* sr
 template <int RT, int DP>
 __global__ void __launch_bounds__(kThreads, 2) prefix_f32_kernel(const __grid_constant__ AttnParams p) {
   using L = Layout<RT, DP>;
-  constexpr int CB = DP / 64;                             // float4 column blocks of O per thread
+  // columns of O per thread: CB blocks of VW neighbours, the blocks 16 VW apart
+  constexpr int VW = DP % 64 ? 2 : 4, CB = DP / (16 * VW), NP = CB * VW / 2;
   extern __shared__ __align__(16) float sm[];
   float *sq = sm + L::Q, *sk = sm + L::K, *sv = sm + L::V, *sp = sm + L::P;
   const Unit x = unit_at(p, blockIdx.x, L::BM, kN);
@@ -89,13 +90,13 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_f32_kernel(const __grid_co
     *reinterpret_cast<float4*>(sq + r * DP + 4 * e) = make_float4(v.x * c, v.y * c, v.z * c, v.w * c);
   }
   float mx[RT], l[RT];
-  uint64_t o[RT][2 * CB];
+  uint64_t o[RT][NP];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     mx[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2 * CB; ++e) o[i][e] = 0;
+    for (int e = 0; e < NP; ++e) o[i][e] = 0;
   }
   for (int step = 0; step < x.steps; ++step) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // K of this step (V may be on its way)
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_f32_kernel(const __grid_co
       l[i] = l[i] * f + sum;                              // (this lane's keys only)
       const uint64_t f2 = pair(f, f);
 #pragma unroll
-      for (int e = 0; e < 2 * CB; ++e) o[i][e] = mul2(o[i][e], f2);
+      for (int e = 0; e < NP; ++e) o[i][e] = mul2(o[i][e], f2);
     }
     __syncthreads();
     if (step + 1 < x.steps)
@@ -154,12 +155,18 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_f32_kernel(const __grid_co
       asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // V of this step
     __syncthreads();
-    // ---- O += P V: columns 4 tx + 64 b
+    // ---- O += P V: columns VW (tx + 16 b) ..
 #pragma unroll 4
     for (int key = 0; key < kN; ++key) {
-      ulonglong2 v[CB];
+      uint64_t v[NP];
 #pragma unroll
-      for (int b = 0; b < CB; ++b) v[b] = *reinterpret_cast<const ulonglong2*>(sv + key * DP + 64 * b + 4 * tx);
+      for (int b = 0; b < CB; ++b) {
+        const float* src = sv + key * DP + VW * (tx + 16 * b);
+        if constexpr (VW == 4)
+          *reinterpret_cast<ulonglong2*>(v + 2 * b) = *reinterpret_cast<const ulonglong2*>(src);
+        else
+          v[b] = *reinterpret_cast<const uint64_t*>(src);
+      }
       float w[RT];
       const float* pr = sp + key * L::BM + ((ty * RT) ^ ((key & (L::BM / 8 - 1)) << 3));
       if constexpr (RT == 8) {
@@ -173,10 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_f32_kernel(const __grid_co
       for (int i = 0; i < RT; ++i) {
         const uint64_t w2 = pair(w[i], w[i]);
 #pragma unroll
-        for (int b = 0; b < CB; ++b) {
-          o[i][2 * b] = fma2(w2, v[b].x, o[i][2 * b]);
-          o[i][2 * b + 1] = fma2(w2, v[b].y, o[i][2 * b + 1]);
-        }
+        for (int e = 0; e < NP; ++e) o[i][e] = fma2(w2, v[e], o[i][e]);
       }
     }
     __syncthreads();
@@ -198,9 +202,12 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_f32_kernel(const __grid_co
     if (tx == 0) p.part_lse[part] = l[i] == 0.f ? -INFINITY : mx[i] + log2f(l[i]);
 #pragma unroll
     for (int b = 0; b < CB; ++b)
-      if (64 * b + 4 * tx < D) {
-        const float2 y = unpair(o[i][2 * b]), z = unpair(o[i][2 * b + 1]);
-        *reinterpret_cast<float4*>(p.part_o + part * D + 64 * b + 4 * tx) = make_float4(y.x * inv, y.y * inv, z.x * inv, z.y * inv);
+      if (VW * (tx + 16 * b) < D) {
+#pragma unroll
+        for (int e = 0; e < VW / 2; ++e) {
+          const float2 y = unpair(o[i][b * VW / 2 + e]);
+          *reinterpret_cast<float2*>(p.part_o + part * D + VW * (tx + 16 * b) + 2 * e) = make_float2(y.x * inv, y.y * inv);
+        }
       }
   }
 }
@@ -216,8 +223,9 @@ tr_status launch(const AttnParams& p, cudaStream_t st) {
 }  // namespace
 
 tr_status launch_prefix_f32(const AttnParams& p, int unit_rows, cudaStream_t st) {
-  if (unit_rows == 64) return p.d.d_head <= 64 ? launch<8, 64>(p, st) : launch<8, 128>(p, st);
-  return p.d.d_head <= 64 ? launch<2, 64>(p, st) : launch<2, 128>(p, st);
+  const int D = p.d.d_head;
+  if (unit_rows == 64) return D <= 64 ? launch<8, 64>(p, st) : D <= 96 ? launch<8, 96>(p, st) : launch<8, 128>(p, st);
+  return D <= 64 ? launch<2, 64>(p, st) : D <= 96 ? launch<2, 96>(p, st) : launch<2, 128>(p, st);
 }
 
 }  // namespace attn
