@@ -358,6 +358,7 @@ size_t tr_prefix_attention_workspace(const tr_attn_desc* desc, const int64_t* se
  * (its tensor-core operand) and computes everything else in fp32; TR_F32 computes in fp32
  * throughout.  The result does not depend on which other requests share the call by more than
  * the rounding of the fp32 sums: the split of a long prefix over SMs goes by the whole batch.
+ * out, lse and workspace overlap nothing else of the call.
  */
 tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q, const int64_t* seq_offsets,
                               const void* k_prefix, const void* v_prefix, const int64_t* prefix_offsets,

@@ -9,9 +9,12 @@
 //     that the loads of the next warps are always in flight.
 //   beam_pick_kernel  one CTA per request: the rows' log-sum-exp (in 64 bits: two beams' totals
 //     are compared across rows), the tiles' best totals, a bound that at least k tiles reach (or
-//     groups, of few tiles; the k-th largest of the threads' own best, by bisection with one
-//     block-wide count per step), and then only the tiles, groups and logits that reach it --
-//     about k of each -- are looked at, the tokens among them cut down the same way and ranked.
+//     groups, of few tiles; the k-th largest of the threads' own best, bisected by one warp), and
+//     then only the tiles, groups and logits that reach it -- about k of each -- are looked at,
+//     the tokens among them cut down the same way and ranked.
+// 64 x 16 rows of 131072 bf16: the sums 48 us (5.6 TB/s, the exponentials' unit 70 % busy), the choice 13 us,
+// a chain of some ten barriers that few threads have work between.  Lists of the best per chunk of a row
+// took 87 us for the first part, rings filled by cp.async under a persistent grid 108.
 // When more tokens reach the bound than the sort holds (long runs of equal logits), the exact k-th
 // candidate is found by bisection over the tokens themselves.
 //
@@ -672,7 +675,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
 // One CTA moves one column slice of one state of one request: every surviving row's slice is
 // loaded into registers before the first is stored, and no other CTA touches the slice, so the
 // move is safe in place whatever the parents are.  Traffic: each row read once (children of one
-// parent read it again from L2) and written once.
+// parent read it again from L2) and written once.  16 states of 32 x 32 rows of 98 KB under random parents:
+// 432 us, of 401 that the 63 % of rows with a child, read, and all rows, written, take at a copy's rate.
 constexpr int kMoveThreads = 256;
 
 struct MoveState {

@@ -236,7 +236,10 @@ tr_status launch_finish(const AttnParams& p, int sms, cudaStream_t st) {
 // lane's 16 bytes of a key are its share of two slices, and of values its share of eight).  P^T
 // turns from a result into an operand by a transpose between lanes.  `parts` warps share a
 // sequence's keys; all meet in shared memory, where the prefix part's results join.  The read of the
-// keys and values bounds it: a warp has 16 of each in flight.
+// keys and values bounds it: a warp has 16 of each in flight.  512 sequences with 61 to 64 tokens, 8 key heads
+// of 128: 127 MB in 40 us, the chain of a CTA (its length, its loads, its products, the merge) times seven
+// waves at the 16 warps per SM that 128 registers leave.  A persistent grid that brings the next unit's rows to
+// L2 meanwhile made the call 127 us instead of 107, the same without the persistent grid 114.
 constexpr int kSuffixThreads = 128;
 
 __device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {

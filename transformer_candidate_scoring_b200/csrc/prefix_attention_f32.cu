@@ -7,7 +7,8 @@
 // scores and 8 x 8 outputs, so that an operand read from shared memory feeds four to eight of
 // them.  The K of the next step is copied while P V runs, the V of this one while S is formed.
 // FMA throughput (2 d_head x 2 per row and key) bounds it for many rows, the read of K and V for
-// few.
+// few.  3 x 37 sequences of 3 query tokens, 6 heads of 80 on 2, prefixes of up to 1501 tokens: 31 us (38 with
+// d_head padded to 128), 216 CTAs of two steps at about one warp per scheduler; the FMA pipes are 23 % busy.
 #include <math.h>
 
 #include <algorithm>

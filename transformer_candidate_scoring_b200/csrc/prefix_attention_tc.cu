@@ -12,17 +12,22 @@
 // and every other step of keys (their results are merged at the unit's end).
 //
 //   TMEM, 512 columns   S/P of tile 0, S/P of tile 1 (128 each), O of tile 0, O of tile 1
-//   shared memory       Q of both tiles, a ring of K steps and one of V steps; all in the
+//   shared memory       Q tiles, a ring of K steps and one of V steps; all in the
 //                       128-byte-swizzled layout (K-major for Q and K; V is [keys][d_head], the
 //                       MN-major form), K and V by TMA, d_head padded to 64 or 128 by TMA's zeros
 //   warps 0-3, 4-7      softmax of tile 0 and 1, one row per thread, and the epilogue
-//   warps 8, 9, 10      K loads, V loads, MMA issue; warp 11 owns the tensor memory
+//   warps 8, 9, 10      K loads, V loads, MMA issue
+//   warp 11             tensor memory; the next unit's Q where shared memory has room for it
 //
 // A step's chain -- S, softmax, P V, of which the next S waits because P lies where S was -- bounds
-// many rows: about 3,600 cycles for both tiles' 128 keys, of which the tensor core is busy 2,048
-// (855 TFLOP/s over 8,192 sequences, 16 heads of 128 on 4 key heads and 4,096 keys).  Steps of 64 keys with two S buffers
+// many rows: 2 x 4,096 sequences with 16 heads of 128 on 4 over 4,096 keys take 286 us (960 TFLOP/s),
+// the tensor core busy 45 % and the exponentials' unit 45 % of it.  Steps of 64 keys with two S buffers
 // per tile, separate S and P with steps of 80 keys, one MMA warp per tile, two threads per row and a part
-// of the exponentials on the FMA pipes measured no faster (319 to 427 us against 322).
+// of the exponentials on the FMA pipes measured no faster (319 to 427 us against 322 of the kernel then).
+// Few rows are bound by the read of K and V: 1 x 16 sequences over 131,072 keys, 268 MB in 51 us.  Short
+// prefixes are bound by what a unit costs once (Q, the first S, the result): 16 x 4,096 sequences with 8
+// heads of 16 over 16 to 128 keys, 14 units per SM, take 75 us, and took 91 with one Q buffer that the softmax
+// warps filled between units.
 //
 // The row maximum that O and l are relative to is raised only when the new one is more than 2^8
 // away (then O is rescaled in TMEM): numerators stay below 2^8 and sums in fp32 range.  Values
@@ -128,7 +133,8 @@ __device__ __forceinline__ uint32_t piece(uint32_t tile, int r, int c) {
 }
 
 // Whether Q has two buffers, so that a unit's rows come while the one before it is worked on: d_head up to
-// 64, or units that all have one tile of rows (kOne).
+// 64 (there the rings leave room for four tiles), or units that all have one tile of rows (kOne; 32 sequences
+// with 4 heads of 128 on each key head over 16 ragged prefixes: 119 -> 112 us).
 template <int DH, bool kOne>
 constexpr bool kQAhead = DH == 64 || kOne;
 // Bytes from one Q buffer to the other.
