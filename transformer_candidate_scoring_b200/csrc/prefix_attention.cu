@@ -232,14 +232,16 @@ tr_status launch_finish(const AttnParams& p, int sms, cudaStream_t st) {
 // The same for bf16 suffixes of eight tokens and more, on warp-level matrix instructions: of the L_t x
 // (n_head / n_kv_head) rows of a sequence that share a key head, eight are the columns of
 // S^T = K Q^T (16 keys x 8 rows) and of O^T += V^T P^T, so each key and value is read once for all of them,
-// straight into the fragments of the products (the order of d_head within a product is free, so a
+// through shared memory, whole rows at a time (the order of d_head within a product is free, so a
 // lane's 16 bytes of a key are its share of two slices, and of values its share of eight).  P^T
 // turns from a result into an operand by a transpose between lanes.  `parts` warps share a
 // sequence's keys; all meet in shared memory, where the prefix part's results join.  The read of the
 // keys and values bounds it: a warp has 16 of each in flight.  512 sequences with 61 to 64 tokens, 8 key heads
-// of 128: 127 MB in 40 us, the chain of a CTA (its length, its loads, its products, the merge) times seven
-// waves at the 16 warps per SM that 128 registers leave.  A persistent grid that brings the next unit's rows to
-// L2 meanwhile made the call 127 us instead of 107, the same without the persistent grid 114.
+// of 128: 127 MB in 33 us, the chain of a CTA (its length, its rows, its products, the merge) times seven
+// waves at 16 warps per SM.  The call took 107 us with the rows read straight into the products' registers, 16
+// bytes of eight rows at a time, against 99; five CTAs per SM at 102 registers 100.5, six with spills 107.
+// With the rows in registers, a persistent grid that brings the next unit's rows to L2 meanwhile took 127,
+// the same without the persistent grid 114.
 constexpr int kSuffixThreads = 128;
 
 __device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -258,7 +260,12 @@ template <int kBlocks, bool kCausal>     // 64-wide blocks of d_head
 __global__ void __launch_bounds__(kSuffixThreads, kBlocks == 1 ? 6 : 4)
 suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, const FastDiv div_tiles, const FastDiv div_chunks) {
   constexpr int DP = kBlocks * 64;
-  __shared__ float s_o[kSuffixThreads / 32][8][DP + 4], s_m[kSuffixThreads / 32][8], s_l[kSuffixThreads / 32][8];
+  // a warp's 16 keys and 16 values, 16-byte piece c of row r at piece c ^ (r & 7); then its result
+  constexpr int kRow = DP * 2, kWarpBytes = 32 * kRow;
+  static_assert(8 * (DP + 4) * 4 <= kWarpBytes, "a warp's result");
+  __shared__ __align__(128) uint8_t s_kv[kSuffixThreads / 32][kWarpBytes];
+  __shared__ float s_m[kSuffixThreads / 32][8], s_l[kSuffixThreads / 32][8];
+  auto s_o = [&](int w, int r, int c) { return reinterpret_cast<float*>(s_kv[w]) + r * (DP + 4) + c; };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, qd = lane % 4;
   const int parts = 1 << log_parts, part = warp & (parts - 1), D = p.d.d_head, H = p.d.n_head, Hk = p.d.n_kv_head;
   const int G = p.group, n_rows = p.d.L_t * G;
@@ -268,6 +275,12 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
   const int row0 = (u - sh * r_tiles) * 8;                 // rows t * G + head in group
   const float c = p.d.scale * kLog2e;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint32_t kv = (uint32_t)__cvta_generic_to_shared(s_kv[warp]);
+  auto piece = [&](int r, int c) {                         // rows 0-15 keys, 16-31 values
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(kv + r * kRow + ((c ^ (r & 7)) << 4)));
+    return v;
+  };
   const int len = visible_suffix(p, s, p.d.L_t - 1);       // what the last query token sees: all of it
   // ---- Q: 16 bytes of row g per 32 columns
   uint4 q[2 * kBlocks];
@@ -290,28 +303,27 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
   float o[4 * kBlocks][4] = {};                            // O^T: 16 columns of d_head x 8 rows
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   for (int j0 = part * 16; j0 < len; j0 += parts * 16) {
-    uint4 k[2][2 * kBlocks], v[4][kBlocks];
+    __syncwarp();                                          // (the rows of the step before have been read)
+    constexpr int kPieces = DP / 8, kRows = 32 / kPieces;  // rows a warp copies at a time
+    {
+      const int c = lane % kPieces;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = j0 + g + 8 * h;
-      const __nv_bfloat16* src = kp + j * p.d.suffix_token + qd * 8;
-#pragma unroll
-      for (int i = 0; i < 2 * kBlocks; ++i)
-        k[h][i] = j < len && i * 32 + qd * 8 < D ? __ldg(reinterpret_cast<const uint4*>(src + i * 32)) : zero;
+      for (int r = lane / kPieces; r < 16; r += kRows) {
+        const int j = j0 + r, bytes = j < len && c * 8 < D ? 16 : 0;            // 0: zeros
+        const int64_t at = bytes ? j * p.d.suffix_token + c * 8 : 0;
+        const uint32_t dst = kv + r * kRow + ((c ^ (r & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kp + at), "r"(bytes) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * kRow), "l"(vp + at), "r"(bytes) : "memory");
+      }
     }
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int j = j0 + 2 * qd + (h & 1) + (h >> 1) * 8;
-      const __nv_bfloat16* src = vp + j * p.d.suffix_token + g * 8;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-        v[h][b] = j < len && b * 64 + g * 8 < D ? __ldg(reinterpret_cast<const uint4*>(src + b * 64)) : zero;
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
     float st[4] = {};                                      // keys g (0, 1) and g + 8 (2, 3) x rows 2 qd, 2 qd + 1
 #pragma unroll
     for (int i = 0; i < 2 * kBlocks; ++i) {
-      mma_16816(st, k[0][i].x, k[1][i].x, k[0][i].y, k[1][i].y, q[i].x, q[i].y);
-      mma_16816(st, k[0][i].z, k[1][i].z, k[0][i].w, k[1][i].w, q[i].z, q[i].w);
+      const uint4 k0 = piece(g, qd + 4 * i), k1 = piece(g + 8, qd + 4 * i);
+      mma_16816(st, k0.x, k1.x, k0.y, k1.y, q[i].x, q[i].y);
+      mma_16816(st, k0.z, k1.z, k0.w, k1.w, q[i].z, q[i].w);
     }
     float f[2];
 #pragma unroll
@@ -334,7 +346,10 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
 #pragma unroll
       for (int h = 0; h < 4; ++h)
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) odd = odd || not_finite(v[h][b].x) || not_finite(v[h][b].y) || not_finite(v[h][b].z) || not_finite(v[h][b].w);
+        for (int b = 0; b < kBlocks; ++b) {
+          const uint4 v = piece(16 + lane / 8 + 4 * h, lane % 8 + 8 * b);
+          odd = odd || not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
+        }
       if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll
         for (int i = 0; i < 4 * kBlocks; ++i)
@@ -360,18 +375,25 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
     }
     const uint32_t b0 = transpose_8x8(bf16x2(st[0], st[1])), b1 = transpose_8x8(bf16x2(st[2], st[3]));
 #pragma unroll
-    for (int i = 0; i < 4 * kBlocks; ++i) {
-      // rows of A: columns 8 g' + 2 i' and + 1 of the block, g' = 0 .. 7 in lanes' order
-      const int b = i / 4, w = i % 4;
-      uint32_t x[4];
+    for (int b = 0; b < kBlocks; ++b) {
+      uint4 v[4];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) x[h] = (&v[h][b].x)[w];
+      for (int h = 0; h < 4; ++h) v[h] = piece(16 + 2 * qd + (h & 1) + (h >> 1) * 8, g + 8 * b);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] *= f[e & 1];
-      mma_16816(o[i], __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x5410),
-                __byte_perm(x[2], x[3], 0x7632), b0, b1);
+      for (int w = 0; w < 4; ++w) {
+        // rows of A: columns 8 g' + 2 w and + 1 of the block, g' = 0 .. 7 in lanes' order
+        const int i = 4 * b + w;
+        uint32_t x[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) x[h] = (&v[h].x)[w];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= f[e & 1];
+        mma_16816(o[i], __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x5410),
+                  __byte_perm(x[2], x[3], 0x7632), b0, b1);
+      }
     }
   }
+  __syncwarp();
   // ---- o[i][0], [1]: column b * 64 + 8 g + 2 w of rows 2 qd, 2 qd + 1; [2], [3]: the next column
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -383,7 +405,7 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-      float* d = &s_o[warp][2 * qd + e][b * 64 + 8 * g];
+      float* d = s_o(warp, 2 * qd + e, b * 64 + 8 * g);
       *reinterpret_cast<float4*>(d) = make_float4(o[4 * b][e], o[4 * b][2 + e], o[4 * b + 1][e], o[4 * b + 1][2 + e]);
       *reinterpret_cast<float4*>(d + 4) = make_float4(o[4 * b + 2][e], o[4 * b + 2][2 + e], o[4 * b + 3][e], o[4 * b + 3][2 + e]);
     }
@@ -410,7 +432,7 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
       x.rescale(fmaxf(x.m, mm), &base);
       const float f = exp2f(mm - base);
       x.l = fmaf(f, s_l[first + i][rr], x.l);
-      const float4 y = *reinterpret_cast<const float4*>(&s_o[first + i][rr][c0]), z = *reinterpret_cast<const float4*>(&s_o[first + i][rr][c0 + 4]);
+      const float4 y = *reinterpret_cast<const float4*>(s_o(first + i, rr, c0)), z = *reinterpret_cast<const float4*>(s_o(first + i, rr, c0 + 4));
       const float w[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) x.o[e] = fmaf(f, w[e], x.o[e]);
