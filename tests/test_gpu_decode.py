@@ -224,6 +224,22 @@ def test_attention_partial_last_wave(api, case):
     agrees(got, x, d ** -0.5, causal)
 
 
+# Several short units per SM, some without any key of the prefix.
+SHORT = [(64, 1), (128, 1), (128, 0), (40, 1), (128, 5), (64, 12)]
+
+
+@pytest.mark.parametrize("d,S", SHORT)
+def test_attention_many_short_prefixes(api, d, S):
+    R, H = 60, 10
+    counts = [(3 * i + 1) % 7 for i in range(R)]
+    prefix = [0 if i % 4 == 1 else (37 * i) % 300 for i in range(R)]
+    L_t = 2 if S else 1
+    x = attn_inputs(19, counts, prefix, H, H, d, S, L_t)
+    got = call(api, dev(x), causal=S > 0)
+    ok(api)
+    agrees(got, x, d ** -0.5, S > 0)
+
+
 RAGGED = [5003, 1, 700, 2049, 4100, 128, 127, 5990, 3333, 129, 64, 2500, 1111, 5500, 900, 0, 4999, 2222]
 RUNS = [
     # counts, prefix, H, H_kv, d, S, L_t, causal
