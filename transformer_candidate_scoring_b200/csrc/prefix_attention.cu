@@ -27,7 +27,7 @@ __device__ __forceinline__ int request_of(const AttnParams& p, int64_t s) {
   return lo;
 }
 
-// The suffix part of every row, and the merge with the prefix part's partial results.  A team of
+// The suffix part of every row (with `simt`, the prefix too), and the merge with the prefix part's partial results.  A team of
 // kLanes lanes holds a row, eight of its columns per lane; `parts` teams share a row's suffix
 // keys and partial results where rows are few (their results meet in shared memory).  What it
 // must read -- each sequence's own keys and values, the partial results -- bounds it: four keys
@@ -133,47 +133,51 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   const RequestPlan& rq = p.req[request_of(p, s)];
   const float c = p.d.scale * kLog2e;
   Running x;
-  if (p.d.suffix_cap > 0) {
+  if (p.d.suffix_cap > 0 || p.simt) {
     float q[8] = {};
     if (in) load8(static_cast<const T*>(p.q) + st * p.d.q_token + (int64_t)h * D + c0, q);
-    const int n = visible_suffix(p, s, t);
-    const int per = (n + parts - 1) / parts, end = min(n, (part + 1) * per);
-    const int steps = __reduce_max_sync(0xffffffffu, max(0, end - part * per));    // of the warp's teams
-    const int64_t so = s * p.d.suffix_seq + hk * p.d.suffix_head + c0;
-    const T *k = static_cast<const T*>(p.k_suffix) + so, *v = static_cast<const T*>(p.v_suffix) + so;
-    constexpr int kAhead = 4;
-    for (int i0 = 0; i0 < steps; i0 += kAhead) {
-      float a[kAhead], vv[kAhead][8];
+#pragma unroll 1
+    for (int own = p.simt ? 0 : 1; own < 2; ++own) {       // the prefix's keys, the sequence's own
+      const int n = own ? visible_suffix(p, s, t) : rq.p1 - rq.p0;
+      const int64_t token = own ? p.d.suffix_token : p.d.prefix_token;
+      const int64_t from = own ? s * p.d.suffix_seq + hk * p.d.suffix_head + c0 : rq.p0 * token + hk * p.d.prefix_head + c0;
+      const T *k = static_cast<const T*>(own ? p.k_suffix : p.k_prefix) + from, *v = static_cast<const T*>(own ? p.v_suffix : p.v_prefix) + from;
+      const int per = (n + parts - 1) / parts, end = min(n, (part + 1) * per);
+      const int steps = __reduce_max_sync(0xffffffffu, max(0, end - part * per));    // of the warp's teams
+      constexpr int kAhead = 4;
+      for (int i0 = 0; i0 < steps; i0 += kAhead) {
+        float a[kAhead], vv[kAhead][8];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int j = part * per + i0 + u;
-        float kk[8] = {};
-        a[u] = 0.f;
-        if (in && j < end) load8(k + j * p.d.suffix_token, kk);
+        for (int u = 0; u < kAhead; ++u) {
+          const int j = part * per + i0 + u;
+          float kk[8] = {};
+          a[u] = 0.f;
+          if (in && j < end) load8(k + j * token, kk);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[u] = fmaf(q[e], kk[e], a[u]);
-      }
+          for (int e = 0; e < 8; ++e) a[u] = fmaf(q[e], kk[e], a[u]);
+        }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int j = part * per + i0 + u;
+        for (int u = 0; u < kAhead; ++u) {
+          const int j = part * per + i0 + u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vv[u][e] = 0.f;
-        if (in && j < end) load8(v + j * p.d.suffix_token, vv[u]);
-      }
+          for (int e = 0; e < 8; ++e) vv[u][e] = 0.f;
+          if (in && j < end) load8(v + j * token, vv[u]);
+        }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-        for (int y = kLanes / 2; y; y >>= 1) a[u] += __shfl_xor_sync(0xffffffffu, a[u], y);
-        a[u] = part * per + i0 + u < end ? a[u] * c : -INFINITY;
-      }
-      float base;
-      x.rescale(fmaxf(fmaxf(fmaxf(x.m, a[0]), fmaxf(a[1], a[2])), a[3]), &base);
+          for (int y = kLanes / 2; y; y >>= 1) a[u] += __shfl_xor_sync(0xffffffffu, a[u], y);
+          a[u] = part * per + i0 + u < end ? a[u] * c : -INFINITY;
+        }
+        float base;
+        x.rescale(fmaxf(fmaxf(fmaxf(x.m, a[0]), fmaxf(a[1], a[2])), a[3]), &base);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const float w = exp2f(a[u] - base);
-        x.l += w;
+        for (int u = 0; u < kAhead; ++u) {
+          const float w = exp2f(a[u] - base);
+          x.l += w;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x.o[e] = fmaf(w, vv[u][e], x.o[e]);
+          for (int e = 0; e < 8; ++e) x.o[e] = fmaf(w, vv[u][e], x.o[e]);
+        }
       }
     }
   }
@@ -587,6 +591,13 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool dir
   p.req[p.R].part = part;
 }
 
+constexpr int kMmaSuffix = 8;      // own tokens from which suffix_kernel takes them (bf16)
+// Prefixes that are all this short are read by finish_kernel, key by key for each row: one launch, no partial
+// results.  Without and with, of 2, 8 and 16 keys: 5 x 459 sequences, 16 heads of 96 on 2, two own keys 43 and 28,
+// 36, 50 us; 16 x 2,048 with 8 heads of 16 38 and 25, 32, 46; 24 x 77 fp32 with 32 heads of 128 on 8 112 and 35, 71,
+// 128; 8 x 8 with 8 heads of 64 9.5 and 5.5, 6.5, 8.7.
+constexpr int kSimtPrefix = 8;
+
 struct Plan {
   bool direct = false;        // the tensor-core kernel writes the results
   size_t bytes = 0;
@@ -610,6 +621,13 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
     q.p1 = (int)prefix[std::min(r + 1, R)];
   }
   TR_TRY(sm_count(&plan.sms));
+  int64_t longest = 0;
+  for (int r = 0; r < R; ++r) longest = std::max(longest, seq[r + 1] > seq[r] ? prefix[r + 1] - prefix[r] : 0);
+  if (longest <= kSimtPrefix && (d->dtype == TR_F32 || d->suffix_cap < kMmaSuffix)) {
+    p.simt = true;
+    p.halves = kNoHalves;
+    return TR_OK;
+  }
   if (d->dtype == TR_F32) {
     // two CTAs per SM; units of 16 rows waste less of the few rows of small batches, units of 64
     // read K and V a quarter as often
@@ -683,7 +701,7 @@ extern "C" tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q
   }
   if (p.n_units > 0) TR_TRY(launch_prefix_tc(p, plan.direct, st));
   if (plan.direct) return TR_OK;
-  if (desc->suffix_cap >= 8) {
+  if (desc->suffix_cap >= kMmaSuffix && !p.simt) {
     if (desc->d_head <= 64) return desc->causal ? launch_suffix<1, true>(p, st) : launch_suffix<1, false>(p, st);
     return desc->causal ? launch_suffix<2, true>(p, st) : launch_suffix<2, false>(p, st);
   }
