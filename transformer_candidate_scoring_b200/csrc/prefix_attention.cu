@@ -211,26 +211,34 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
   if (p.lse && tl == 0) p.lse[row] = x.lse();
 }
 
+int finish_lanes(int D) { return D <= 8 ? 1 : D <= 16 ? 2 : D <= 32 ? 4 : D <= 64 ? 8 : 16; }
+// Teams per row: several while there are few rows and enough keys or partial results to share, about 16 warps per SM.
+int finish_parts(const AttnParams& p, int sms, bool simt) {
+  const int lanes = finish_lanes(p.d.d_head);
+  int parts = 1, items = p.d.suffix_cap;
+  for (int r = 0; r < p.R; ++r) items = std::max(items, simt ? p.req[r].p1 - p.req[r].p0 : p.req[r].n_split);
+  while (parts < 16 && parts * 2 <= kFinishThreads / lanes && items > 4 * parts &&
+         p.n_rows * lanes * parts * 2 <= (int64_t)sms * 16 * 32)
+    parts *= 2;
+  return parts;
+}
+
 template <typename T, int kLanes>
 tr_status launch_finish(const AttnParams& p, int sms, cudaStream_t st) {
-  // several teams per row while there are few rows and enough to share: about 16 warps per SM
-  int parts = 1, items = p.d.suffix_cap;
-  for (int r = 0; r < p.R; ++r) items = std::max(items, p.req[r].n_split);
-  while (parts < 16 && parts * 2 <= kFinishThreads / kLanes && items > 4 * parts &&
-         p.n_rows * kLanes * parts * 2 <= (int64_t)sms * 16 * 32)
-    parts *= 2;
+  const int parts = finish_parts(p, sms, p.simt);
   const int rows_per = kFinishThreads / kLanes / parts;
   return launch_dependent(p.n_units > 0, finish_kernel<T, kLanes>, (unsigned)((p.n_rows + rows_per - 1) / rows_per), kFinishThreads, 0, st,
                           "finish_kernel", p, parts);
 }
 template <typename T>
 tr_status launch_finish(const AttnParams& p, int sms, cudaStream_t st) {
-  const int D = p.d.d_head;
-  return D <= 8    ? launch_finish<T, 1>(p, sms, st)
-         : D <= 16 ? launch_finish<T, 2>(p, sms, st)
-         : D <= 32 ? launch_finish<T, 4>(p, sms, st)
-         : D <= 64 ? launch_finish<T, 8>(p, sms, st)
-                   : launch_finish<T, 16>(p, sms, st);
+  switch (finish_lanes(p.d.d_head)) {
+    case 1: return launch_finish<T, 1>(p, sms, st);
+    case 2: return launch_finish<T, 2>(p, sms, st);
+    case 4: return launch_finish<T, 4>(p, sms, st);
+    case 8: return launch_finish<T, 8>(p, sms, st);
+    default: return launch_finish<T, 16>(p, sms, st);
+  }
 }
 
 // The same for bf16 suffixes of eight tokens and more, on warp-level matrix instructions: of the L_t x
@@ -274,7 +282,7 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
   const int parts = 1 << log_parts, part = warp & (parts - 1), D = p.d.d_head, H = p.d.n_head, Hk = p.d.n_kv_head;
   const int G = p.group, n_rows = p.d.L_t * G;
   const int n_unit = p.req[p.R].s0 * Hk * r_tiles;         // below 2^31: no more than query rows
-  const int u_at = ((int)blockIdx.x * (kSuffixThreads / 32) + warp) >> log_parts, u = min(u_at, n_unit - 1);
+  const int u_at = (int)(((int64_t)blockIdx.x * (kSuffixThreads / 32) + warp) >> log_parts), u = min(u_at, n_unit - 1);
   const int sh = fast_div(u, div_tiles), s = fast_div(sh, p.div_kv), hk = sh - s * Hk;
   const int row0 = (u - sh * r_tiles) * 8;                 // rows t * G + head in group
   const float c = p.d.scale * kLog2e;
@@ -302,19 +310,25 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
   for (int e = 0; e < 2; ++e)
     seen[e] = kCausal ? max(0, len - max(0, p.d.L_t - 1 - fast_div(row0 + 2 * qd + e, p.div_g))) : len;
   const int seen_by_all = kCausal ? max(0, len - (p.d.L_t - 1 - fast_div(row0, p.div_g))) : len;
-  const int64_t so = (int64_t)s * p.d.suffix_seq + hk * p.d.suffix_head;
-  const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(p.k_suffix) + so, *vp = static_cast<const __nv_bfloat16*>(p.v_suffix) + so;
+  const RequestPlan& rq = p.req[request_of(p, s)];
+  const int pre = p.simt ? rq.p1 - rq.p0 : 0, pre_steps = (pre + 15) / 16, steps = pre_steps + (len + 15) / 16;
   float o[4 * kBlocks][4] = {};                            // O^T: 16 columns of d_head x 8 rows
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  for (int j0 = part * 16; j0 < len; j0 += parts * 16) {
+  for (int i = part; i < steps; i += parts) {              // of 16 keys: with simt, the prefix's, then the sequence's own
+    const bool own = i >= pre_steps;
+    const int j0 = (own ? i - pre_steps : i) * 16, n = own ? len : pre;
+    const int64_t token = own ? p.d.suffix_token : p.d.prefix_token;
+    const int64_t from = own ? (int64_t)s * p.d.suffix_seq + hk * p.d.suffix_head : rq.p0 * token + hk * p.d.prefix_head;
+    const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(own ? p.k_suffix : p.k_prefix) + from;
+    const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(own ? p.v_suffix : p.v_prefix) + from;
     __syncwarp();                                          // (the rows of the step before have been read)
     constexpr int kPieces = DP / 8, kRows = 32 / kPieces;  // rows a warp copies at a time
     {
       const int c = lane % kPieces;
 #pragma unroll
       for (int r = lane / kPieces; r < 16; r += kRows) {
-        const int j = j0 + r, bytes = j < len && c * 8 < D ? 16 : 0;            // 0: zeros
-        const int64_t at = bytes ? j * p.d.suffix_token + c * 8 : 0;
+        const int j = j0 + r, bytes = j < n && c * 8 < D ? 16 : 0;              // 0: zeros
+        const int64_t at = bytes ? j * token + c * 8 : 0;
         const uint32_t dst = kv + r * kRow + ((c ^ (r & 7)) << 4);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kp + at), "r"(bytes) : "memory");
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * kRow), "l"(vp + at), "r"(bytes) : "memory");
@@ -332,7 +346,8 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
     float f[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float a0 = j0 + g < seen[e] ? st[e] * c : -INFINITY, a1 = j0 + g + 8 < seen[e] ? st[2 + e] * c : -INFINITY;
+      const int sees = own ? seen[e] : n;
+      const float a0 = j0 + g < sees ? st[e] * c : -INFINITY, a1 = j0 + g + 8 < sees ? st[2 + e] * c : -INFINITY;
       float top = fmaxf(m[e], fmaxf(a0, a1));
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -345,7 +360,7 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
     }
     // Of keys that only the later of the rows see, the product's 0 x V of the others is 0 unless V is
     // infinite or NaN: then every row adds the keys it sees, one by one.
-    if (kCausal && j0 + 16 > seen_by_all && len > seen_by_all) {
+    if (kCausal && own && j0 + 16 > seen_by_all && len > seen_by_all) {
       bool odd = false;
 #pragma unroll
       for (int h = 0; h < 4; ++h)
@@ -366,7 +381,7 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) {
             float y[8] = {};
-            if (b * 64 + g * 8 < D) load8(vp + (j0 + jj) * p.d.suffix_token + b * 64 + g * 8, y);
+            if (b * 64 + g * 8 < D) load8(vp + (j0 + jj) * token + b * 64 + g * 8, y);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
               if (j0 + jj < seen[e])
@@ -418,7 +433,6 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
   __syncthreads();
   // ---- eight columns of a row per thread: the warps' results, then the prefix part's
   if (u_at >= n_unit) return;
-  const RequestPlan& rq = p.req[request_of(p, s)];
   const int64_t rows = (int64_t)(rq.s1 - rq.s0) * p.d.L_t * H;
   const int chunks = D / 8, first = warp - part, n_results = results_of(p, rq);
   const int items = min(8, n_rows - row0) * chunks;
@@ -457,13 +471,19 @@ suffix_kernel(const __grid_constant__ AttnParams p, int log_parts, int r_tiles, 
 }
 
 template <int kBlocks, bool kCausal>
-tr_status launch_suffix(const AttnParams& p, cudaStream_t st) {
-  // a warp per 16 keys or per eight results of the prefix, up to the four of a CTA
-  int steps = (p.d.suffix_cap + 15) / 16;
-  for (int r = 0; r < p.R; ++r) steps = std::max(steps, p.req[r].n_split / 8);
-  const int log_parts = steps >= 4 ? 2 : steps >= 2 ? 1 : 0;
-  const int r_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 7) / 8, units = (kSuffixThreads / 32) >> log_parts;
+tr_status launch_suffix(const AttnParams& p, int sms, cudaStream_t st) {
+  const int r_tiles = (p.d.L_t * (p.d.n_head / p.d.n_kv_head) + 7) / 8;
   const int64_t n_unit = (int64_t)p.req[p.R].s0 * p.d.n_kv_head * r_tiles;
+  // a warp per 16 own keys or per eight results of the prefix, up to the four of a CTA; where these leave warps
+  // to spare, one per 16 keys of the prefix too (with simt)
+  int steps = (p.d.suffix_cap + 15) / 16, keys = 0;
+  for (int r = 0; r < p.R; ++r) {
+    steps = std::max(steps, p.req[r].n_split / 8);
+    if (p.simt && p.req[r].s1 > p.req[r].s0) keys = std::max(keys, p.req[r].p1 - p.req[r].p0);
+  }
+  int log_parts = steps >= 4 ? 2 : steps >= 2 ? 1 : 0;
+  while (log_parts < 2 && (2 << log_parts) <= steps + ceil_div(keys, 16) && (n_unit << log_parts) <= (int64_t)sms * 8) ++log_parts;
+  const int units = (kSuffixThreads / 32) >> log_parts;
   return launch_dependent(p.n_units > 0, suffix_kernel<kBlocks, kCausal>, (unsigned)((n_unit + units - 1) / units), kSuffixThreads, 0, st, "suffix_kernel", p,
                           log_parts, r_tiles, fast_div_by((uint32_t)r_tiles), fast_div_by((uint32_t)(p.d.d_head / 8)));
 }
@@ -504,7 +524,8 @@ tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t
 // merge's launch (about 4 us), and requests without a prefix have one (empty) unit per 256 rows.
 // With `runs`, equal runs of steps are a candidate too, at a unit more per CTA: 16 requests of 2048 to 8192 tokens
 // and 32 sequences take 107 us by runs and 122 without, the 18 requests at kUnitSteps 45 and 50.
-void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool direct, bool runs) {
+// Returns the cost.
+double plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool direct, bool runs) {
   const int G = p.d.n_head / p.d.n_kv_head;
   int steps[TR_MAX_REQUESTS], n_m[TR_MAX_REQUESTS];
   int longest = 0;
@@ -556,6 +577,7 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool dir
     const double cost = run * (two ? 2.0 : 1.0) + kUnitSteps + (double)rows_all * split * p.d.d_head * 8.0 / 3.5e6 +
                         (direct ? 6.0 : 0.0);
     if (cost < best_cost) {
+      best_cost = cost;
       p.run = run;
       p.div_run = fast_div_by((uint32_t)run);
       p.n_units = n * p.d.n_kv_head;
@@ -589,14 +611,43 @@ void plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool dir
     p.n_units = unit + rest;
   }
   p.req[p.R].part = part;
+  return longest > 0 ? best_cost : 0.0;
 }
 
 constexpr int kMmaSuffix = 8;      // own tokens from which suffix_kernel takes them (bf16)
-// Prefixes that are all this short are read by finish_kernel, key by key for each row: one launch, no partial
-// results.  Without and with, of 2, 8 and 16 keys: 5 x 459 sequences, 16 heads of 96 on 2, two own keys 43 and 28,
-// 36, 50 us; 16 x 2,048 with 8 heads of 16 38 and 25, 32, 46; 24 x 77 fp32 with 32 heads of 128 on 8 112 and 35, 71,
-// 128; 8 x 8 with 8 heads of 64 9.5 and 5.5, 6.5, 8.7.
-constexpr int kSimtPrefix = 8;
+
+// Whether the kernel of the own keys reads the prefixes too, row by row or sequence by sequence: one launch and no
+// partial results, but keys are read again for every row (finish_kernel) or sequence (suffix_kernel).  In us, the prefix
+// kernel's cost is 3 and 0.74 (fp32: 1.8) per step of the plan's, and 8 bytes per partial result; finish_kernel takes
+// 3.1 ps (fp32: 8.6) per key and lane of a row or 0.27 us (0.45) per key in turn, and 5 us and 25 ps per lane beside; suffix_kernel
+// 0.6 ns (d_head up to 64: 0.4) per 16 keys of a sequence and key head.  Without and with:
+//   16 x 300 sequences, 16 heads of 128 on 8, 23 own keys, prefixes of 2, 32, 64 keys    190 and 154, 175, 221 us
+//   4 x 4, 8 heads of 128, 40 own keys, prefixes of 2, 64, 128                           11.5 and 4.2, 5.2, 6.1
+//   5 x 459, 16 heads of 96 on 2, two own keys, prefixes of 2, 8, 16                     43 and 28, 36, 50
+//   24 x 77 fp32, 32 heads of 128 on 8, none, prefixes of 2, 8, 16                       112 and 35, 71, 128
+bool take_simt(AttnParams& p, int sms, double cost, bool direct) {
+  const tr_attn_desc& d = p.d;
+  const bool f32 = d.dtype == TR_F32, mma = !f32 && d.suffix_cap >= kMmaSuffix;
+  const int lanes = finish_lanes(d.d_head), tiles = ceil_div((int64_t)d.L_t * p.group, 8);
+  double simt = 0.0;
+  int longest = 0, split = 0;
+  for (int r = 0; r < p.R; ++r) {
+    const RequestPlan& q = p.req[r];
+    const int keys = q.s1 > q.s0 ? q.p1 - q.p0 : 0;
+    longest = std::max(longest, keys);
+    split = std::max(split, q.n_split);
+    simt += mma ? (double)(q.s1 - q.s0) * d.n_kv_head * tiles * ceil_div(keys, 16) * (d.d_head > 64 ? 0.6e-3 : 0.4e-3)
+                : (double)request_rows(p, r) * lanes * keys * (f32 ? 8.6e-6 : 3.1e-6);
+  }
+  simt = mma ? simt + 0.2 * ceil_div(longest, 16) : std::max(simt, (f32 ? 0.45 : 0.27) * ceil_div(longest, finish_parts(p, sms, true)));
+  if (direct) simt += 5.0 + 2.5e-5 * p.n_rows * lanes;
+  const double partial = direct || split > 1 ? 0.0 : (double)p.n_rows * d.d_head * 8.0 / 3.5e6;
+  if (longest > 0 && simt >= 3.0 + (f32 ? 1.8 : 0.74) * (cost + partial)) return false;
+  p.simt = true;
+  p.n_units = p.run = 0;
+  for (int r = 0; r < p.R; ++r) p.req[r].n_split = 0;
+  return true;
+}
 
 struct Plan {
   bool direct = false;        // the tensor-core kernel writes the results
@@ -621,27 +672,25 @@ tr_status make_plan(const tr_attn_desc* d, const int64_t* seq, const int64_t* pr
     q.p1 = (int)prefix[std::min(r + 1, R)];
   }
   TR_TRY(sm_count(&plan.sms));
-  int64_t longest = 0;
-  for (int r = 0; r < R; ++r) longest = std::max(longest, seq[r + 1] > seq[r] ? prefix[r + 1] - prefix[r] : 0);
-  if (longest <= kSimtPrefix && (d->dtype == TR_F32 || d->suffix_cap < kMmaSuffix)) {
-    p.simt = true;
-    p.halves = kNoHalves;
-    return TR_OK;
-  }
   if (d->dtype == TR_F32) {
     // two CTAs per SM; units of 16 rows waste less of the few rows of small batches, units of 64
     // read K and V a quarter as often
     int64_t most = 0;
     for (int r = 0; r < R; ++r) most = std::max(most, (seq[r + 1] - seq[r]) * d->L_t * (d->n_head / d->n_kv_head));
     plan.unit_rows = most <= 32 ? 16 : 64;
-    plan_units(p, plan.unit_rows, kStepKeysF32, 2 * plan.sms, false, false);
+    const double cost = plan_units(p, plan.unit_rows, kStepKeysF32, 2 * plan.sms, false, false);
+    if (take_simt(p, plan.sms, cost, false)) return TR_OK;
     plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);
     return TR_OK;
   }
   plan.unit_rows = kUnitRows;
-  plan_units(p, kUnitRows, kStepKeys, plan.sms, d->suffix_cap <= kDirectSuffix, true);
+  const double cost = plan_units(p, kUnitRows, kStepKeys, plan.sms, d->suffix_cap <= kDirectSuffix, true);
   plan.direct = d->suffix_cap <= kDirectSuffix && p.run == 0;
   for (int r = 0; r < R; ++r) plan.direct = plan.direct && (p.req[r].n_split == 1 || p.req[r].s0 == p.req[r].s1);
+  if (take_simt(p, plan.sms, cost, plan.direct)) {
+    plan.direct = false;
+    return TR_OK;
+  }
   if (!plan.direct) plan.bytes = (size_t)p.req[R].part * (d->d_head + 1) * sizeof(float);
   return TR_OK;
 }
@@ -701,9 +750,9 @@ extern "C" tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q
   }
   if (p.n_units > 0) TR_TRY(launch_prefix_tc(p, plan.direct, st));
   if (plan.direct) return TR_OK;
-  if (desc->suffix_cap >= kMmaSuffix && !p.simt) {
-    if (desc->d_head <= 64) return desc->causal ? launch_suffix<1, true>(p, st) : launch_suffix<1, false>(p, st);
-    return desc->causal ? launch_suffix<2, true>(p, st) : launch_suffix<2, false>(p, st);
+  if (desc->suffix_cap >= kMmaSuffix) {
+    if (desc->d_head <= 64) return desc->causal ? launch_suffix<1, true>(p, plan.sms, st) : launch_suffix<1, false>(p, plan.sms, st);
+    return desc->causal ? launch_suffix<2, true>(p, plan.sms, st) : launch_suffix<2, false>(p, plan.sms, st);
   }
   return launch_finish<__nv_bfloat16>(p, plan.sms, st);
 }
