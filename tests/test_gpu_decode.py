@@ -240,6 +240,18 @@ def test_attention_many_short_prefixes(api, d, S):
     agrees(got, x, d ** -0.5, S > 0)
 
 
+@pytest.mark.parametrize("d,S", [(64, 1), (128, 1), (128, 0), (40, 0), (128, 9), (64, 3)])
+def test_attention_many_units_of_one_tile(api, d, S):
+    """The same with more rows each, up to 60 per key head."""
+    R, H = 60, 10
+    counts = [(13 * i) % 60 + 1 for i in range(R)]
+    prefix = [0 if i % 4 == 1 else (37 * i) % 300 + 100 for i in range(R)]
+    x = attn_inputs(20, counts, prefix, H, H, d, S)
+    got = call(api, dev(x))
+    ok(api)
+    agrees(got, x, d ** -0.5, False)
+
+
 RAGGED = [5003, 1, 700, 2049, 4100, 128, 127, 5990, 3333, 129, 64, 2500, 1111, 5500, 900, 0, 4999, 2222]
 RUNS = [
     # counts, prefix, H, H_kv, d, S, L_t, causal

@@ -7,7 +7,8 @@
 // with m, l and o carried from key to key (a new maximum rescales l and o), so that no score is
 // ever stored.  Exponentials are powers of two: a_j is kept times log2(e).  The prefix part runs
 // once per request for all of its sequences (prefix_attention_tc.cu, prefix_attention_f32.cu) and
-// leaves one or, of a split prefix, several normalised partial results per row.
+// leaves one or, of a split prefix, several normalised partial results per row; short prefixes and small
+// batches do without it.
 #include <math.h>
 
 #include <algorithm>
@@ -519,8 +520,8 @@ tr_status check_offsets(const tr_attn_desc* d, const int64_t* seq, const int64_t
 }
 
 // How many steps of keys a unit takes.  Fewer steps give more units to spread over the `slots` (SMs,
-// or CTAs that share one), but every unit costs about three more (kUnitSteps) and every chunk of a prefix a partial result per row.  The candidates are: no split, and
-// the shortest chunks that give one, two or four units per slot.  With `direct`, no split also saves the
+// or CTAs that share one), but every unit costs kUnitSteps more and every chunk of a prefix a partial
+// result per row.  The candidates are: no split, and the shortest chunks that give one, two or four units per slot.  With `direct`, no split also saves the
 // merge's launch (about 4 us), and requests without a prefix have one (empty) unit per 256 rows.
 // With `runs`, equal runs of steps are a candidate too, at a unit more per CTA: 16 requests of 2048 to 8192 tokens
 // and 32 sequences take 107 us by runs and 122 without, the 18 requests at kUnitSteps 45 and 50.
