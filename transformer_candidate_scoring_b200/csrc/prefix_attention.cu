@@ -118,7 +118,7 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int64_t row, int 
 }
 
 template <typename T, int kLanes>
-__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ AttnParams p, int parts) {
+__global__ void __launch_bounds__(kFinishThreads, 3) finish_kernel(const __grid_constant__ AttnParams p, int parts) {
   __shared__ float s_ml[kFinishThreads / kLanes][2];
   __shared__ float s_o[8][kFinishThreads];
   const int team = threadIdx.x / kLanes, tl = threadIdx.x % kLanes;
@@ -542,7 +542,10 @@ double plan_units(AttnParams& p, int unit_rows, int step_keys, int slots, bool d
   }
   auto units = [&](int c) {
     int64_t n = 0;
-    for (int r = 0; r < p.R; ++r) n += (int64_t)p.d.n_kv_head * n_m[r] * ceil_div(steps[r], c);
+    for (int r = 0; r < p.R; ++r) {
+      const int chunks = ceil_div(steps[r], c);
+      n += (int64_t)p.d.n_kv_head * n_m[r] * (direct && c >= longest ? std::max(chunks, 1) : chunks);
+    }
     return n;
   };
   int best = std::max(longest, 1);
@@ -620,12 +623,13 @@ constexpr int kMmaSuffix = 8;      // own tokens from which suffix_kernel takes 
 // Whether the kernel of the own keys reads the prefixes too, row by row or sequence by sequence: one launch and no
 // partial results, but keys are read again for every row (finish_kernel) or sequence (suffix_kernel).  In us, the prefix
 // kernel's cost is 3 and 0.74 (fp32: 1.8) per step of the plan's, and 8 bytes per partial result; finish_kernel takes
-// 3.1 ps (fp32: 8.6) per key and lane of a row or 0.27 us (0.45) per key in turn, and 5 us and 25 ps per lane beside; suffix_kernel
+// 3.1 ps (fp32: 4.5) per key and lane of a row or 0.27 us per key in turn, and 5 us and 25 ps per lane beside; suffix_kernel
 // 0.6 ns (d_head up to 64: 0.4) per 16 keys of a sequence and key head.  Without and with:
 //   16 x 300 sequences, 16 heads of 128 on 8, 23 own keys, prefixes of 2, 32, 64 keys    190 and 154, 175, 221 us
 //   4 x 4, 8 heads of 128, 40 own keys, prefixes of 2, 64, 128                           11.5 and 4.2, 5.2, 6.1
-//   5 x 459, 16 heads of 96 on 2, two own keys, prefixes of 2, 8, 16                     43 and 28, 36, 50
-//   24 x 77 fp32, 32 heads of 128 on 8, none, prefixes of 2, 8, 16                       112 and 35, 71, 128
+//   5 x 459, 16 heads of 96 on 2, two own keys, prefixes of 2, 8                         43 and 28, 34
+//   24 x 77 fp32, 32 heads of 128 on 8, none, prefixes of 2, 8, 16                       112 and 32, 49, 83
+//   1 x 4, 8 heads of 64, four own keys, prefixes of 2, 64, 200                          8.8 and 4.7, 5.0, 6.9
 bool take_simt(AttnParams& p, int sms, double cost, bool direct) {
   const tr_attn_desc& d = p.d;
   const bool f32 = d.dtype == TR_F32, mma = !f32 && d.suffix_cap >= kMmaSuffix;
@@ -638,9 +642,9 @@ bool take_simt(AttnParams& p, int sms, double cost, bool direct) {
     longest = std::max(longest, keys);
     split = std::max(split, q.n_split);
     simt += mma ? (double)(q.s1 - q.s0) * d.n_kv_head * tiles * ceil_div(keys, 16) * (d.d_head > 64 ? 0.6e-3 : 0.4e-3)
-                : (double)request_rows(p, r) * lanes * keys * (f32 ? 8.6e-6 : 3.1e-6);
+                : (double)request_rows(p, r) * lanes * keys * (f32 ? 4.5e-6 : 3.1e-6);
   }
-  simt = mma ? simt + 0.2 * ceil_div(longest, 16) : std::max(simt, (f32 ? 0.45 : 0.27) * ceil_div(longest, finish_parts(p, sms, true)));
+  simt = mma ? simt + 0.2 * ceil_div(longest, 16) : std::max(simt, 0.27 * ceil_div(longest, finish_parts(p, sms, true)));
   if (direct) simt += 5.0 + 2.5e-5 * p.n_rows * lanes;
   const double partial = direct || split > 1 ? 0.0 : (double)p.n_rows * d.d_head * 8.0 / 3.5e6;
   if (longest > 0 && simt >= 3.0 + (f32 ? 1.8 : 0.74) * (cost + partial)) return false;
