@@ -1,0 +1,54 @@
+"""The decode calls on the GPU where their arithmetic or their buffers come to an edge: logits of
+large size."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_decode import DT, api, check_select, ok, select_reference  # noqa: F401  (api: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ selection
+# Tolerances are check_select's: beside the errors named there, the exponent of a term, a difference of
+# two numbers that are each rounded to 24 bits, is up to 64 in size where logits are near 1e9, so it is off by
+# 2^-18 at most, and a total by ln 2 times that; 64-bit totals near 1e9 are off by 2^-22.
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1000, 20001])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [1e4, 1e5, 1e6, 1e7, 7e7, 8e7, 1e8, 9e8, 1e9, 1.1e9, 1e12])
+def test_select_logits_of_large_size(api, size, sign, V, dtype):
+    """Rows whose largest logits are far from zero: all tokens equal, a spread of a few units around the
+    value, a few representable steps around it, and tokens of ordinary size beside it (the value as a
+    mask, or as the only token that counts)."""
+    g = torch.Generator().manual_seed(V)
+    m = sign * size
+    x = torch.full((6, V), m)
+    x[1] += 3 * torch.randn(V, generator=g)
+    x[2] *= 1 + torch.randint(-3, 4, (V,), generator=g) * torch.finfo(DT[dtype]).eps
+    x[3] = torch.where(torch.rand(V, generator=g) < 0.5, torch.randn(V, generator=g), x[3])
+    x[4, 1:] = torch.randn(V - 1, generator=g)
+    x[5] = 2 * torch.randn(V, generator=g)
+    x = x.to(DT[dtype])
+    # a request per row: each row's totals; then all rows as beams of one request, nearly level
+    cum = -torch.rand(6, 1, generator=g)
+    got = api.beam_select(x.cuda(), cum.cuda(), 20)
+    ok(api)
+    check_select(got, select_reference(x, cum, 20), 20)
+    assert (got[0] == 0).all()
+    got = api.beam_select(x.cuda(), cum.view(1, 6).cuda(), 200)
+    ok(api)
+    check_select(got, select_reference(x, cum.view(1, 6), 200), 200)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fill", [-1e8, -1e9])
+def test_select_row_filled_with_a_mask_value(api, fill, dtype):
+    """A beam whose tokens were all filled with the usual mask value offers them as equals."""
+    V, k = 300, 256
+    x = torch.full((1, V), fill).to(DT[dtype])
+    par, tok, sc = api.beam_select(x.cuda(), torch.tensor([[-1.5]]).cuda(), k)
+    ok(api)
+    assert par[0].tolist() == [0] * k and tok[0].tolist() == list(range(k))
+    assert (sc.double().cpu() - (-1.5 - math.log(V))).abs().max() <= 2.0 ** -16

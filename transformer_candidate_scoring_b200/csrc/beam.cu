@@ -85,25 +85,29 @@ __device__ __forceinline__ bool row_offers(const SelectParams& p, int64_t row) {
 // Sums of exponentials are held as sum_i 2^(x_i log2 e - ref), ref the rounded log2 of the
 // largest term m: subtracting a whole number costs the exponent one rounding of its own size,
 // where a subtraction of m log2 e would shift all terms alike by its rounding and so move one
-// beam's total against another's.  The low part of log2 e is applied to the sum, as 2^(m lo); what
-// is left of it, (x_i - m) lo, is below 2^-22 for every term that counts.  Logits beyond 1e9 in size are
-// further apart than any exponential reaches: there the sum counts the largest logit's copies
-// (infinite ones too).
+// beam's total against another's.  log2 e is used as hi + lo, hi its fp32 value.  Terms are formed with hi;
+// with M the row's maximum, x_i lo = M lo + (x_i - M) lo, and
+//     log sum_i exp(x_i) = M + ln 2 (ref - M hi + log2 sum_i 2^(x_i hi - ref) 2^((x_i - M) lo))
+// where M hi is exact in 64 bits, whatever M's size.  The last factor is applied as sums are joined, for the maximum m
+// of each partial sum in x_i's place (m - M is below 200 in size wherever a sum counts, so 1 + (m - M) lo ln 2 is it to
+// 2^-37); what is left, (x_i - m) lo, is below 2^-22 for every term that counts.  Logits beyond 1e9 in size
+// are further apart than any exponential reaches: there the sum counts the largest logit's copies (infinite ones
+// too).
 constexpr float kHuge = 1e9f;
 constexpr float kL2eHi = 1.4426950408889634f;                 // rounds to 1.44269502...
 constexpr float kL2eLo = (float)(1.4426950408889634 - (double)kL2eHi);
 __device__ __forceinline__ bool huge(float m) { return fabsf(m) > kHuge; }
 __device__ __forceinline__ float sum_ref(float m) { return rintf(m * kL2eHi); }
-// The factor that takes a sum relative to `m` to one relative to `to` (to >= m): a power of two, 0
-// or 1, so exact; terms below 2^-126 of the largest are dropped.
+// The factor that takes a sum of largest term `m` to one of largest term `to` (to >= m): a power of two and
+// the low part of log2 e; terms below 2^-126 of the largest are dropped.
 __device__ __forceinline__ float sum_scale(float m, float to) {
   if (m == to) return 1.f;
   if (m == -INFINITY || huge(m) || huge(to)) return 0.f;
   const float n = sum_ref(m) - sum_ref(to);
-  return n < -126.f ? 0.f : __int_as_float((127 + (int)n) << 23);
+  return n < -126.f ? 0.f : fmaf(m - to, kL2eLo * 0.693147f, 1.f) * __int_as_float((127 + (int)n) << 23);
 }
-__device__ __forceinline__ double log_sum(float m, double sum) {   // log sum_i exp(x_i)
-  return huge(m) ? (double)m + log(sum) : 0.6931471805599453 * ((double)sum_ref(m) + log2(sum));
+__device__ __forceinline__ double log_sum(float m, double sum) {   // log sum_i exp(x_i), less m
+  return huge(m) ? log(sum) : 0.6931471805599453 * (((double)sum_ref(m) - (double)m * (double)kL2eHi) + log2(sum));
 }
 
 __device__ __forceinline__ uint64_t pack2f(float x, float y) {
@@ -249,7 +253,6 @@ __global__ void __launch_bounds__(kSumThreads, 4) beam_sum_kernel(const __grid_c
           if (y == y) s += ex2(fmaf(y, kL2eHi, ref));
         }
     }
-    s *= fmaf(m, kL2eLo * 0.693147f, 1.f);
   } else if (m > -INFINITY) {                           // (of all -inf the sum is unused)
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   const int64_t row0 = (int64_t)r * p.W;
   const TileSum* sums = p.sums + row0 * p.n_tile;
   cudaGridDependencySynchronize();
-  // ---- a warp per beam: the row's maximum and sum, then a thread per beam: its log-sum-exp
+  // ---- a warp per beam: the row's maximum and sum, then a thread per beam: its log-sum-exp, less the maximum
   for (int b = warp; b < p.W; b += kWarps) {
     constexpr int kHeld = 4;                            // tiles per lane held between the two steps
     float4 y[kHeld];                                    // (unwritten where the row offers nothing)
@@ -383,15 +386,15 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   __syncthreads();
   if (tid < p.W) {
     const float M = s_max[tid];
-    const double lse = s_kind[tid] != 1 ? 0.0 : huge(M) ? log(s_lse[tid]) : log_sum(M, s_lse[tid]);
+    const double lse = s_kind[tid] != 1 ? 0.0 : log_sum(M, s_lse[tid]);
     s_lse[tid] = lse;
-    s_off[tid] = (float)(s_cum[tid] - (s_kind[tid] != 1 || huge(M) ? lse : lse - (double)M));
+    s_off[tid] = (float)(s_cum[tid] - lse);
   }
   __syncthreads();
   // ---- totals.  Exactly, as a 64-bit key (0: not a candidate):
   auto key_of = [&](int b, float x) -> unsigned long long {
     const float M = s_max[b];
-    const double d = huge(M) ? (x == M ? 0.0 : (double)x - (double)M) : (double)x;
+    const double d = x == M ? 0.0 : (double)x - (double)M;
     const double t = s_cum[b] + (d - s_lse[b]);
     return t > -INFINITY ? okey(t) : 0ull;
   };
