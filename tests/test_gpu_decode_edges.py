@@ -52,3 +52,30 @@ def test_select_row_filled_with_a_mask_value(api, fill, dtype):
     ok(api)
     assert par[0].tolist() == [0] * k and tok[0].tolist() == list(range(k))
     assert (sc.double().cpu() - (-1.5 - math.log(V))).abs().max() <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,k", [(50, 8), (50, 70), (9000, 256), (40000, 100)])
+def test_select_totals_outside_fp32(api, V, k, dtype):
+    """Totals below fp32's range are finite in 64 bits: such a token is still a candidate, in its place,
+    and its score is -inf, the total rounded to fp32.  -inf itself offers nothing."""
+    g = torch.Generator().manual_seed(V)
+    low = -3.3e38 * torch.rand(2, V, generator=g)
+    x = low.clone()
+    x[0, 3], x[1, V // 2] = 3e38, math.inf                  # the second row: +inf leaves the others a total of -inf
+    x[0, 5] = -math.inf
+    x = x.to(DT[dtype])
+    y = torch.stack([torch.zeros(V), low[1]]).to(DT[dtype])
+    for logits, cum in ((x, torch.tensor([[-1.0, -0.5]])), (y, torch.tensor([[-3.4e38, -2e38]]))):
+        got = api.beam_select(logits.cuda(), cum.cuda(), k)
+        ok(api)
+        want = select_reference(logits, cum, k)[0][:k]
+        n = len(want)
+        assert got[0][0].tolist() == [w[1] for w in want] + [-1] * (k - n)
+        assert got[1][0].tolist() == [w[3] for w in want] + [-1] * (k - n)
+        total = torch.tensor([w[0] for w in want] + [-math.inf] * (k - n), dtype=torch.float64)
+        assert (total[:n] > -math.inf).all()
+        score, rounded = got[2][0].cpu(), total.float()
+        assert torch.equal(score == -math.inf, rounded == -math.inf)
+        at = rounded > -math.inf
+        assert ((score[at].double() - total[at]).abs() <= 2.0 ** -16 + 2.0 ** -23 * total[at].abs()).all()

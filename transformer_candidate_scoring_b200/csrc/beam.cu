@@ -399,11 +399,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     return t > -INFINITY ? okey(t) : 0ull;
   };
   // In fp32, t, off by at most e: a difference and a sum of two terms, each of which was rounded
-  // once, so 2^-22 of their sizes covers them.
+  // once, so 2^-22 of their sizes covers them.  A difference or a sum below fp32's range counts as its lowest
+  // value: t + e is still no less than the total, and t - e is -inf.
   struct Near { float t, e; };
   auto near_of = [&](int b, float x) -> Near {
-    const float M = s_max[b], off = s_off[b], d = x == M ? 0.f : x - M;
-    return Near{d + off, 0x1p-22f * (fabsf(d) + fabsf(off))};
+    const float M = s_max[b], off = s_off[b], d = x == M ? 0.f : fmaxf(x - M, -FLT_MAX);
+    return Near{fmaxf(d + off, -FLT_MAX), 0x1p-22f * (fabsf(d) + fabsf(off))};
   };
   const int per_row = p.n_tile * 32, n_tile = p.W * p.n_tile, n_group = p.W * per_row;
   const float* best = p.best + row0 * per_row;
@@ -559,10 +560,11 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       const uint4 q = p.aligned ? load_vec<T, 16>(lr, v, p.V) : load_partial<T>(lr + v, p.V - v);
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
       const uint32_t bits = p.allowed ? allowed_bits(p, row0 + b, v) : ~0u;
+      const float above = s_max[b] == INFINITY ? FLT_MAX : -INFINITY;    // beside +inf, the others' totals are -inf
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const float x = P::at(w[e / (N / 4)], e);
-        if (x > -INFINITY && (bits >> e & 1u)) {
+        if (x > above && (bits >> e & 1u)) {
           const Near y = near_of(b, x);
           if (y.t + y.e >= bound) f(b, x, v + e);
         }
