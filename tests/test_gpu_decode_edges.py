@@ -1,11 +1,11 @@
 """The decode calls on the GPU where their arithmetic or their buffers come to an edge: logits of
-large size."""
+large size, buffers of calls on other streams."""
 import math
 
 import pytest
 import torch
 
-from test_gpu_decode import DT, api, check_select, ok, select_reference  # noqa: F401  (api: a fixture)
+from test_gpu_decode import DT, api, attn_inputs, call, check_select, dev, ok, select_reference  # noqa: F401  (api: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,51 @@ def test_select_totals_outside_fp32(api, V, k, dtype):
         assert torch.equal(score == -math.inf, rounded == -math.inf)
         at = rounded > -math.inf
         assert ((score[at].double() - total[at]).abs() <= 2.0 ** -16 + 2.0 ** -23 * total[at].abs()).all()
+
+
+# ------------------------------------------------------------------ streams
+def _choose(api, x, **kw):
+    return api.beam_select(x["logits"], x["cum"], 20, **kw)
+
+
+def _stream_inputs(what, seed):
+    if what == "attention":
+        return dev(attn_inputs(seed, [33, 20], [1500, 900], 8, 2, 128, 7))
+    g = torch.Generator().manual_seed(seed)
+    return {"logits": torch.randn(32, 30000, generator=g).cuda(), "cum": -torch.rand(4, 8, generator=g).cuda()}
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("what,run", [("attention", call), ("selection", _choose)])
+def test_buffers_of_a_call_on_another_stream(api, what, run, handle):
+    """Results and workspace of a call on a side stream share no memory with blocks that the current stream
+    still works on, whether freed before the call or after its results were used."""
+    x, y = _stream_inputs(what, 1), _stream_inputs(what, 2)
+    want, other = run(api, x), run(api, y)
+    ok(api)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    torch.cuda.empty_cache()
+    # blocks of every size that the call may ask for, freed while the current stream has yet to fill them
+    sizes = [t.numel() * t.element_size() for t in want] + [1 << n for n in range(8, 25)]
+    torch.cuda._sleep(100_000_000)
+    held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in held]
+    for t in held:
+        t.fill_(255)
+    del held, t
+    got = run(api, x, stream=stream)
+    assert not any(a <= t.data_ptr() < b for t in got for a, b in spans)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # results that the current stream has yet to read, freed, and a second call
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(100_000_000)
+    kept = [t.clone() for t in got]
+    del got
+    again = run(api, y, stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(kept, want))
+    assert all(torch.equal(a, b) for a, b in zip(again, other))
+    ok(api)

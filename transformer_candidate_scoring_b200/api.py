@@ -279,11 +279,22 @@ def _run(dev: int, stream, call, *args) -> None:
 
 
 def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
-    """A buffer on the device of ``like`` from torch's allocator for work on ``stream`` (None: the current
-    one), kept from reuse until that work is done."""
-    t = like.new_empty(shape, dtype=dtype)
+    """A buffer on the device of ``like`` for work on ``stream`` (None: the current one), out of that stream's
+    share of torch's allocator: what the block held before was freed behind work of the same stream."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, like.get_device())
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _result(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """The same for a result: kept from reuse until the caller's current stream has run what uses it, too."""
+    t = _new(like, shape, dtype, stream)
     if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.get_device()))
+        t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
@@ -377,13 +388,13 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
         _layout(q), _layout(k_prefix), _layout(v_prefix), _layout(k_suffix), _layout(v_suffix), _layout(suffix_len),
         tuple(map(int, prefix_offsets)), tuple(map(int, seq_offsets)), None if scale is None else float(scale), bool(causal), dev)
     if out is None:
-        out = torch.empty_like(q) if stream is None and q.is_contiguous() else _new(q, q.shape, q.dtype, stream)
+        out = torch.empty_like(q) if stream is None and q.is_contiguous() else _result(q, q.shape, q.dtype, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out: expected q's shape and type")
     else:
         _ptr(out)
     if lse is None:
-        lse = _new(q, q.shape[:-1], torch.float32, stream)
+        lse = _result(q, q.shape[:-1], torch.float32, stream)
     elif lse.shape != q.shape[:-1] or lse.dtype != torch.float32:
         raise ValueError("lse: expected fp32 of q's shape without the last dimension")
     else:
@@ -440,11 +451,11 @@ def beam_select(logits: torch.Tensor, cum: torch.Tensor, k: int, *, finished: to
                 raise ValueError(f"{name}: expected {dt} [R, k]")
             _ptr(t)
     if parent is None:
-        parent = _new(logits, (R, k), torch.int32, stream)
+        parent = _result(logits, (R, k), torch.int32, stream)
     if token is None:
-        token = _new(logits, (R, k), torch.int32, stream)
+        token = _result(logits, (R, k), torch.int32, stream)
     if score is None:
-        score = _new(logits, (R, k), torch.float32, stream)
+        score = _result(logits, (R, k), torch.float32, stream)
     ws, size = _workspace(workspace, need, logits, stream)
     _run(dev, stream, L.load().tr_beam_select, logits.data_ptr(), code, ld, _ptr(cum), _ptr(finished),
          None if allowed is None else allowed.data_ptr(), allowed_ld, R, W, V, k, int(pad_token), parent.data_ptr(), token.data_ptr(),
