@@ -419,6 +419,10 @@ typedef struct {
 } tr_beam_state;
 tr_status tr_beam_reorder(const tr_beam_state* states, int n_states, const int32_t* parent, int R, int W_in,
                           int W_out, tr_stream stream);
+/* The refusals above over any number of states, on the host; launches nothing.  For states that
+ * take several calls: their calls run one after the other, so a dst of one of them must not
+ * share bytes with a src or dst of the others either. */
+tr_status tr_beam_reorder_check(const tr_beam_state* states, int n_states, int R, int W_in, int W_out);
 
 /*
  * No-allocation variant of tr_prefill_user.  The paper has no counterpart: this entry point

@@ -127,3 +127,40 @@ def test_buffers_of_a_call_on_another_stream(api, what, run, handle):
     assert all(torch.equal(a, b) for a, b in zip(kept, want))
     assert all(torch.equal(a, b) for a, b in zip(again, other))
     ok(api)
+
+
+# ------------------------------------------------------------------ reordering
+def test_reorder_refuses_conflicts_among_many_states(api):
+    """Over 64 states: one listed twice, an out that is another's state, two equal outs, wherever they stand,
+    are refused before anything moves; K and V of joint caches, and states read twice, are not."""
+    R, W, n = 2, 3, 150
+    par = torch.tensor([[1, 2, 0], [2, 2, 1]], dtype=torch.int32).cuda()
+    rows = torch.tensor([1, 2, 0, 5, 5, 4])
+    init = torch.arange(n * R * W * 5, dtype=torch.float32).view(n, R * W, 5)
+
+    def fresh():
+        return list(init.cuda().unbind(0)), list(torch.zeros(n, R * W, 5, device="cuda").unbind(0))
+    for i, j in ((0, 1), (0, 64), (63, 64), (2, 149), (70, 140), (149, 5)):
+        st, out = fresh()
+        twice = list(st)
+        twice[j] = st[i]
+        with pytest.raises(api.TrError):
+            api.beam_reorder(twice, par)
+        into = list(out)
+        into[i] = st[j]
+        with pytest.raises(api.TrError):
+            api.beam_reorder(st, par, outs=into)
+        same = list(out)
+        same[i] = out[j]
+        with pytest.raises(api.TrError):
+            api.beam_reorder(st, par, outs=same)
+        ok(api)
+        assert torch.equal(torch.stack(st).cpu(), init) and not torch.stack(out).any()
+        got = api.beam_reorder(twice, par, outs=out)             # read twice
+        ok(api)
+        assert torch.equal(got[j].cpu(), init[i][rows]) and torch.equal(got[i].cpu(), init[i][rows])
+    joint = torch.arange(40 * R * W * 2 * 5, dtype=torch.float32).view(40, R * W, 2, 5)
+    d = joint.cuda()
+    api.beam_reorder([d[i, :, kv] for i in range(40) for kv in range(2)], par)
+    ok(api)
+    assert torch.equal(d.cpu(), joint[:, rows])

@@ -481,7 +481,8 @@ def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor, outs: Seq
     """tr_beam_reorder: row r*W_out + i of every state becomes row r*W_in + parent[r, i] (int32
     [R, W_out]); a negative parent leaves the row as it was.  states: tensors [R*W_in, ...] of any
     type, each row contiguous (cache[:, :len] moves the filled part).  In place without ``outs``;
-    else into outs [R*W_out, ...].  Any number of states."""
+    else into outs [R*W_out, ...].  Any number of states, none of whose rows another's may overlap
+    but where both are only read."""
     states = list(states)
     dsts = states if outs is None else list(outs)
     if parent.dim() != 2 or parent.dtype != torch.int32:
@@ -506,11 +507,13 @@ def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor, outs: Seq
                 raise ValueError(f"state {i}: expected rows [R*W_in, ...] and an out [R*W_out, ...]")
             last = layout
         flat += (o.data_ptr(), s.data_ptr(), o_stride, stride, row_bytes)
-    call, par = L.load().tr_beam_reorder, _ptr(parent)
-    for i in range(0, len(states), L.TR_MAX_STATES):
-        m = min(L.TR_MAX_STATES, len(states) - i)
-        packed = struct.pack("=" + "QQqqq" * m, *flat[5 * i:5 * (i + m)])
-        _run(dev, stream, call, packed, m, par, R, W_in, W_out)
+    lib, par, n = L.load(), _ptr(parent), len(states)
+    packed = struct.pack("=" + "QQqqq" * n, *flat)
+    if n > L.TR_MAX_STATES:               # (several calls: what one moves, another must not read)
+        _check(lib.tr_beam_reorder_check(packed, n, R, W_in, W_out))
+    for i in range(0, n, L.TR_MAX_STATES):
+        m, size = min(L.TR_MAX_STATES, n - i), C.sizeof(L.BeamState)
+        _run(dev, stream, lib.tr_beam_reorder, packed[i * size:(i + m) * size] if m < n else packed, m, par, R, W_in, W_out)
     return dsts
 
 
