@@ -402,8 +402,9 @@ tr_status tr_beam_select(const void* logits, tr_dtype logits_dtype, int64_t ld, 
  *     dst row r*W_out + i  =  src row r*W_in + parent[r*W_out + i]
  * A negative parent leaves its dst row as it was; one >= W_in does too and sets the device
  * status word (TR_ERR_KEY_RANGE).  dst == src reorders in place (then W_in == W_out and the row
- * strides are equal); a dst that shares bytes with any other src or dst of the call is refused
- * (rows interleaved at one stride, like the K and V of a joint cache, share none).
+ * strides are equal); a dst that shares bytes with any other src or dst of the call, or with
+ * parent, is refused (rows interleaved at one stride, like the K and V of a joint cache, share
+ * none).
  *   states  HOST array [n_states] (<= TR_MAX_STATES); any dtype: rows are row_bytes bytes
  *   parent  DEVICE int32 [R][W_out]
  * 1 <= W_in, W_out <= TR_MAX_BEAMS, R * W < 2^20.  When every address, stride and row_bytes of
@@ -422,7 +423,8 @@ tr_status tr_beam_reorder(const tr_beam_state* states, int n_states, const int32
 /* The refusals above over any number of states, on the host; launches nothing.  For states that
  * take several calls: their calls run one after the other, so a dst of one of them must not
  * share bytes with a src or dst of the others either. */
-tr_status tr_beam_reorder_check(const tr_beam_state* states, int n_states, int R, int W_in, int W_out);
+tr_status tr_beam_reorder_check(const tr_beam_state* states, int n_states, const int32_t* parent, int R, int W_in,
+                                int W_out);
 
 /*
  * No-allocation variant of tr_prefill_user.  The paper has no counterpart: this entry point

@@ -164,3 +164,11 @@ def test_reorder_refuses_conflicts_among_many_states(api):
     api.beam_reorder([d[i, :, kv] for i in range(40) for kv in range(2)], par)
     ok(api)
     assert torch.equal(d.cpu(), joint[:, rows])
+
+
+def test_reorder_refuses_its_own_parent(api):
+    par = torch.tensor([[1, 2, 0], [2, 2, 1]], dtype=torch.int32).cuda()
+    with pytest.raises(api.TrError):
+        api.beam_reorder([par.view(6)], par)
+    ok(api)
+    assert par.tolist() == [[1, 2, 0], [2, 2, 1]]

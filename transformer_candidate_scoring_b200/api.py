@@ -510,7 +510,7 @@ def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor, outs: Seq
     lib, par, n = L.load(), _ptr(parent), len(states)
     packed = struct.pack("=" + "QQqqq" * n, *flat)
     if n > L.TR_MAX_STATES:               # (several calls: what one moves, another must not read)
-        _check(lib.tr_beam_reorder_check(packed, n, R, W_in, W_out))
+        _check(lib.tr_beam_reorder_check(packed, n, par, R, W_in, W_out))
     for i in range(0, n, L.TR_MAX_STATES):
         m, size = min(L.TR_MAX_STATES, n - i), C.sizeof(L.BeamState)
         _run(dev, stream, lib.tr_beam_reorder, packed[i * size:(i + m) * size] if m < n else packed, m, par, R, W_in, W_out)

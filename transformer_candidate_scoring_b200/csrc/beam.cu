@@ -815,13 +815,15 @@ tr_status check_select(int R, int W, int V, int k) {
   return TR_OK;
 }
 
-tr_status check_reorder(const tr_beam_state* states, int n_states, int R, int W_in, int W_out) {
+tr_status check_reorder(const tr_beam_state* states, int n_states, const int32_t* parent, int R, int W_in, int W_out) {
   if (n_states < 0) return fail(TR_ERR_INVALID_ARG, "n_states=%d", n_states);
   if (W_in < 1 || W_in > TR_MAX_BEAMS || W_out < 1 || W_out > TR_MAX_BEAMS)
     return fail(TR_ERR_INVALID_ARG, "W_in=%d, W_out=%d (need 1..%d)", W_in, W_out, TR_MAX_BEAMS);
   if (R < 1 || (int64_t)R * std::max(W_in, W_out) >= (1 << 20))
     return fail(TR_ERR_INVALID_ARG, "R=%d (need R >= 1 and R*W < 2^20)", R);
-  if (n_states > 0 && !states) return fail(TR_ERR_INVALID_ARG, "null pointer");
+  if (n_states > 0 && (!states || !parent)) return fail(TR_ERR_INVALID_ARG, "null pointer");
+  if ((uintptr_t)parent % 4) return fail(TR_ERR_INVALID_ARG, "parent is not aligned to its type");
+  const Rows par{parent, W_out * 4ll, W_out * 4ll, R};
   for (int i = 0; i < n_states; ++i) {
     const tr_beam_state& s = states[i];
     if (s.row_bytes < 0 || (s.row_bytes > 0 && (!s.dst || !s.src)))
@@ -830,6 +832,8 @@ tr_status check_reorder(const tr_beam_state* states, int n_states, int R, int W_
       return fail(TR_ERR_INVALID_ARG, "state %d: stride below row_bytes or too large", i);
     if (s.dst == s.src && (W_in != W_out || s.dst_stride != s.src_stride))
       return fail(TR_ERR_INVALID_ARG, "state %d: in place needs W_in == W_out and equal strides", i);
+    if (overlap(Rows{s.dst, s.dst_stride, s.row_bytes, (int64_t)R * W_out}, par))
+      return fail(TR_ERR_INVALID_ARG, "state %d: dst overlaps parent", i);
     for (int j = 0; j < i + 1 && s.row_bytes > 0; ++j) {
       const tr_beam_state& o = states[j];
       const Rows sd{s.dst, s.dst_stride, s.row_bytes, (int64_t)R * W_out}, ss{s.src, s.src_stride, s.row_bytes, (int64_t)R * W_in};
@@ -895,17 +899,16 @@ extern "C" tr_status tr_beam_select(const void* logits, tr_dtype logits_dtype, i
   return logits_dtype == TR_F32 ? launch_select<float>(p, R, align, st) : launch_select<__nv_bfloat16>(p, R, align, st);
 }
 
-extern "C" tr_status tr_beam_reorder_check(const tr_beam_state* states, int n_states, int R, int W_in, int W_out) {
-  return check_reorder(states, n_states, R, W_in, W_out);
+extern "C" tr_status tr_beam_reorder_check(const tr_beam_state* states, int n_states, const int32_t* parent, int R, int W_in,
+                                           int W_out) {
+  return check_reorder(states, n_states, parent, R, W_in, W_out);
 }
 
 extern "C" tr_status tr_beam_reorder(const tr_beam_state* states, int n_states, const int32_t* parent, int R, int W_in,
                                      int W_out, tr_stream stream) {
   if (n_states > TR_MAX_STATES) return fail(TR_ERR_INVALID_ARG, "n_states=%d (need 0..%d)", n_states, TR_MAX_STATES);
-  TR_TRY(check_reorder(states, n_states, R, W_in, W_out));
+  TR_TRY(check_reorder(states, n_states, parent, R, W_in, W_out));
   if (n_states == 0) return TR_OK;
-  if (!parent) return fail(TR_ERR_INVALID_ARG, "null pointer");
-  if ((uintptr_t)parent % 4) return fail(TR_ERR_INVALID_ARG, "parent is not aligned to its type");
   MoveParams p{};
   uintptr_t align = 0;
   for (int i = 0; i < n_states; ++i) {
