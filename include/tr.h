@@ -354,10 +354,13 @@ size_t tr_prefix_attention_workspace(const tr_attn_desc* desc, const int64_t* se
  *   lse            DEVICE fp32 [n][L_t][n_head], contiguous, or NULL
  *   workspace      DEVICE, 16-byte aligned, at least tr_prefix_attention_workspace() bytes, the
  *                  call's own until it has run
- * 1 <= R <= TR_MAX_REQUESTS.  TR_BF16 rounds the softmax numerators of a value product to bf16
- * (its tensor-core operand) and computes everything else in fp32; TR_F32 computes in fp32
- * throughout.  The result does not depend on which other requests share the call by more than
- * the rounding of the fp32 sums: the split of a long prefix over SMs goes by the whole batch.
+ * 1 <= R <= TR_MAX_REQUESTS.  TR_F32 computes in fp32 throughout.  TR_BF16 may round the softmax
+ * numerators of a value product to bf16 (a tensor-core operand) and computes everything else in
+ * fp32.  Which kernels read a request's keys, and where a long prefix is cut, goes by the whole
+ * batch, so a request's result may change with the requests beside it: by the rounding of fp32
+ * sums and, with TR_BF16, by that of the numerators before and after, at most
+ *     2^-7 sum_j exp(a_j - lse) |v_j|
+ * in out before its own rounding (lse has no part in it).  The same call gives the same bits.
  * out, lse and workspace overlap nothing else of the call.
  */
 tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q, const int64_t* seq_offsets,

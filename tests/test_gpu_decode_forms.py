@@ -233,3 +233,30 @@ def test_form_offsets_beyond_32_bits(api, dtype, form, counts, prefix, S):
     got = call(api, y)
     ok(api)
     agrees(got, formula(x, d ** -0.5, False))
+
+
+# The first request alone and beside others, which take it to another form or cut its keys in other places.  Each result is
+# within its tolerance of the formula, so the two are within twice that of one another: twice the fp32 terms and, in
+# bf16, 2^-7 sum_j p_j |v_j| for the numerators and 2^-7 |out| for the results.
+BESIDE = [("bf16", "own", "merge", 32, 64, [32] * 15, [64] * 15, 8, 8, 64, 4), ("bf16", "own", "merge", 32, 64, [1], [8000], 8, 8, 64, 4),
+          ("bf16", "own", "merge", 32, 64, [1], [8000], 8, 8, 128, 20), ("bf16", "merge", "merge", 40, 4001, [40] * 20, [2222] * 20, 8, 4, 128, 9),
+          ("bf16", "merge", "direct", 300, 2000, [2000] * 3, [2000] * 3, 16, 8, 64, 1), ("f32", "own", "merge", 32, 64, [1], [8000], 8, 8, 64, 4),
+          ("f32", "merge", "merge", 40, 4001, [40] * 20, [2222] * 20, 8, 4, 80, 9)]
+
+
+@pytest.mark.parametrize("case", BESIDE, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}x{c[4]}-{c[7]}x{c[8]}x{c[9]}")
+def test_form_request_alone_and_beside_others(api, case):
+    dtype, alone, beside, count, prefix, counts, prefixes, H, H_kv, d, S = case
+    x = dev(attn_inputs(3, [count, *counts], [prefix, *prefixes], H, H_kv, d, S, 1, dtype))
+    y = {z: x[z][:n] for z, n in (("q", count), ("k", prefix), ("v", prefix), ("ks", count), ("vs", count), ("sl", count))}
+    y.update(so=x["so"][:2], po=x["po"][:2])
+    assert form_of(api, y, False) == alone and form_of(api, x, False) == beside
+    one, all_, again = call(api, y), call(api, x), call(api, x)
+    ok(api)
+    assert all(torch.equal(a, b) for a, b in zip(all_, again))
+    want = formula(y, d ** -0.5, False)
+    part = [z[:count] for z in all_]
+    agrees(one, want)
+    agrees(part, want)
+    for a, b, tol in zip(one, part, want[2:]):
+        assert bool(((a.double() - b.double()).abs() <= 2 * tol).all())

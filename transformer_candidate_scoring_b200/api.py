@@ -382,7 +382,8 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     prefix_offsets[r+1]-1 of k_prefix, v_prefix [T, H_kv, d] (any token and head strides) and to
     the first suffix_len[s] (int32) tokens of their own k_suffix, v_suffix [n, S, H_kv, d];
     with ``causal``, query token t to L_t - 1 - t fewer of those.  ``scale`` defaults to
-    1 / sqrt(d).  bf16 or fp32.  Buffers that are not given are allocated."""
+    1 / sqrt(d).  bf16 or fp32.  Buffers that are not given are allocated.  A request's result may
+    change with the requests beside it, by rounding (in bf16 of the softmax numerators too)."""
     dev = _on(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_len, out, lse)
     desc, so, po, R, S, need = _attention_plan(
         _layout(q), _layout(k_prefix), _layout(v_prefix), _layout(k_suffix), _layout(v_suffix), _layout(suffix_len),
