@@ -341,7 +341,7 @@ size_t tr_prefix_attention_workspace(const tr_attn_desc* desc, const int64_t* se
 /*
  *   q              DEVICE [n][L_t][n_head][d_head], 16-byte aligned
  *   seq_offsets    HOST int64 [R+1]: sequences of request r are seq_offsets[r] .. [r+1]-1;
- *                  starts at 0, non-decreasing, ends at n (n * L_t < 2^31)
+ *                  starts at 0, non-decreasing, ends at n (n * L_t * n_head < 2^31)
  *   k_prefix, v_prefix  DEVICE [prefix_offsets[R]][n_kv_head][d_head], 16-byte aligned (may be
  *                  NULL when there is no prefix token)
  *   prefix_offsets HOST int64 [R+1]: prefix tokens of request r; starts at 0 or later (the
@@ -372,7 +372,9 @@ tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q, const int
  * Beam selection: the k best continuations of every request over its W beams and the vocabulary.
  *     total(b, v) = cum[b] + logits[b][v] - log sum_u exp(logits[b][u])
  * Best first.  Totals are compared in 64 bits; equal totals go by lower beam, then higher logit,
- * then lower token.
+ * then lower token.  The exponentials of the sum are fp32, which moves all totals of a beam
+ * alike, by less than 2^-16 (beams of equal logits by the same): candidates of one beam are in
+ * their exact order, and those of two beams may change places where they are nearer than that.
  *   logits     DEVICE [R*W][V] of logits_dtype, `ld` elements from row to row (rows at 16-byte
  *              aligned addresses are read fastest)
  *   cum        DEVICE fp32 [R*W]: a beam's log probability so far; a beam whose value is not
@@ -385,11 +387,12 @@ tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q, const int
  *              whole vocabulary; finished beams are not masked
  *   parent, token  DEVICE int32 [R][k]: beam within the request, token; -1, -1 where fewer than
  *              k continuations have a total above -inf
- *   score      DEVICE fp32 [R][k]: the total (padding -inf)
+ *   score      DEVICE fp32 [R][k]: the total (padding -inf); with k == W it may be cum itself
  * A NaN logit counts as -inf; a row with +inf logits gives its whole probability to them in
  * equal parts; a row of -inf offers nothing.  1 <= W <= TR_MAX_BEAMS, 1 <= k <= TR_MAX_BEAM_K,
  * 1 <= V <= 2^24, 0 <= pad_token < 2^24, R * W < 2^20.  The result depends on nothing but the
- * request's own rows.  workspace: DEVICE, 16-byte aligned, tr_beam_select_workspace() bytes, the
+ * request's own rows.  But for that score, the outputs and the workspace overlap nothing else of
+ * the call.  workspace: DEVICE, 16-byte aligned, tr_beam_select_workspace() bytes, the
  * call's own until it has run (SIZE_MAX: invalid sizes, tr_last_error() says why).
  */
 #define TR_MAX_BEAMS 256

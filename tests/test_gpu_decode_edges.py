@@ -1,5 +1,5 @@
-"""The decode calls on the GPU where their arithmetic or their buffers come to an edge: logits of
-large size, buffers of calls on other streams."""
+"""The decode calls on the GPU where their arithmetic, their sizes or their buffers come to an edge:
+logits of large size, the longest rows, buffers of calls on other streams, states that overlap."""
 import math
 
 import pytest
@@ -79,6 +79,53 @@ def test_select_totals_outside_fp32(api, V, k, dtype):
         assert torch.equal(score == -math.inf, rounded == -math.inf)
         at = rounded > -math.inf
         assert ((score[at].double() - total[at]).abs() <= 2.0 ** -16 + 2.0 ** -23 * total[at].abs()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W,V,k", [(2, 1 << 24, 256), (256, 1 << 17, 256), (256, 160001, 100), (1, (1 << 24) - 5, 7)])
+def test_select_largest_sizes(api, W, V, k, dtype):
+    """The reference is check_select's, formed on the GPU: the k + 50 best totals of each call in 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(V + W)
+    x = (torch.randn(W, V, generator=g, device="cuda") * 2).to(DT[dtype])
+    x[:, V - 1] = 9.0                                        # the last token is among the best
+    cum = -2 * torch.rand(1, W, generator=g, device="cuda")
+    got = api.beam_select(x, cum, k)
+    ok(api)
+    found = []
+    for b in range(W):
+        y = x[b].double()
+        lse = torch.logsumexp(y, 0)
+        top = torch.topk(y, k).values[-1]
+        at = torch.nonzero(y >= top).view(-1)
+        found += [(float(cum[0, b]) + float(y[v] - lse), b, float(y[v]), int(v)) for v in at[torch.argsort(-y[at], stable=True)[:k + 50]]]
+    found.sort(key=lambda c: (-c[0], c[1], -c[2], c[3]))
+    check_select(got, [found], k)
+
+
+def test_select_nothing_to_offer(api):
+    """Requests whose beams are all dead, or whose masks allow nothing, beside one that offers."""
+    R, W, V, k = 4, 3, 9000, 5
+    x = torch.randn(R * W, V, generator=torch.Generator().manual_seed(2))
+    cum = torch.full((R, W), -math.inf)
+    cum[1], cum[3] = -1.0, -2.0
+    words = torch.full((R * W, -(-V // 32)), -1, dtype=torch.int32)
+    words[9:] = 0
+    got = api.beam_select(x.cuda(), cum.cuda(), k, allowed=words.cuda())
+    ok(api)
+    check_select(got, select_reference(x, cum, k, None, (words != 0).repeat_interleave(32, 1)[:, :V]), k)
+    for r in (0, 2, 3):
+        assert got[0][r].tolist() == got[1][r].tolist() == [-1] * k and torch.isneginf(got[2][r]).all()
+
+
+def test_select_score_over_cum(api):
+    """With k == W the score may be cum itself."""
+    R, W, V = 6, 5, 3000
+    x = torch.randn(R * W, V, generator=torch.Generator().manual_seed(4)).cuda()
+    cum = -torch.rand(R, W, generator=torch.Generator().manual_seed(5)).cuda()
+    want = api.beam_select(x, cum, W)
+    got = api.beam_select(x, cum, W, score=cum)
+    ok(api)
+    assert got[2].data_ptr() == cum.data_ptr() and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 # ------------------------------------------------------------------ streams
@@ -172,3 +219,23 @@ def test_reorder_refuses_its_own_parent(api):
         api.beam_reorder([par.view(6)], par)
     ok(api)
     assert par.tolist() == [[1, 2, 0], [2, 2, 1]]
+
+
+@pytest.mark.parametrize("row", [(1 << 30) + 48, (1 << 28) + 4])
+def test_reorder_rows_and_states_beyond_32_bits(api, row):
+    """Rows of a gigabyte and a state of several, in place; then rows of another state 2^32 bytes apart."""
+    R, W = 2, 3
+    x = torch.randint(-2**31, 2**31, (R * W, row // 4), dtype=torch.int32, device="cuda")
+    ends = [0, row // 8, row // 4 - 1]
+    before, sums = x[:, ends].clone(), x.sum(1)
+    par = torch.tensor([[1, 2, 0], [2, 2, 1]], dtype=torch.int32).cuda()
+    rows = torch.tensor([1, 2, 0, 5, 5, 4]).cuda()
+    api.beam_reorder([x], par)
+    ok(api)
+    assert torch.equal(x[:, ends], before[rows]) and torch.equal(x.sum(1), sums[rows])
+    del x
+    far = torch.empty(5 * (1 << 30) + 64, dtype=torch.int32, device="cuda").as_strided((R * W, 16), (1 << 30, 1))
+    far.copy_(torch.arange(96, dtype=torch.int32).view(6, 16))
+    api.beam_reorder([far], par)
+    ok(api)
+    assert torch.equal(far.cpu(), torch.arange(96, dtype=torch.int32).view(6, 16)[rows.cpu()])

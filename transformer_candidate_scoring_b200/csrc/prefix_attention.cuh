@@ -63,7 +63,7 @@ struct AttnParams {
   int* status;
   tr_attn_desc d;
   int R, n_units;      // (with runs, the CTAs)
-  bool simt;           // no prefix kernel: finish_kernel reads the prefixes too
+  bool simt;           // no prefix kernel: the kernel of the own keys reads the prefixes too
   int halves;          // from this unit on, each is two of half the rows (kNoHalves: none)
   int run;             // steps per CTA, 0: units of `chunk` steps
   int64_t n_rows;      // query rows of all requests: n * L_t * n_head
