@@ -373,8 +373,8 @@ tr_status tr_prefix_attention(const tr_attn_desc* desc, const void* q, const int
  *     total(b, v) = cum[b] + logits[b][v] - log sum_u exp(logits[b][u])
  * Best first.  Totals are compared in 64 bits; equal totals go by lower beam, then higher logit,
  * then lower token.  The exponentials of the sum are fp32, which moves all totals of a beam
- * alike, by less than 2^-16 (beams of equal logits by the same): candidates of one beam are in
- * their exact order, and those of two beams may change places where they are nearer than that.
+ * alike, by less than 2^-17 (beams of equal logits by the same): candidates of one beam are in
+ * their exact order, and those of two beams may change places where they are nearer than 2^-16.
  *   logits     DEVICE [R*W][V] of logits_dtype, `ld` elements from row to row (rows at 16-byte
  *              aligned addresses are read fastest)
  *   cum        DEVICE fp32 [R*W]: a beam's log probability so far; a beam whose value is not
