@@ -727,8 +727,7 @@ tr_status encode_map(CUtensorMap* map, const void* base, const AttnParams& p) {
   auto encode = get_encode();
   if (!encode) return fail(TR_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const int64_t row = p.d.d_head;
-  const int tokens = std::max(p.req[p.R].p0, 1);
-  if (p.req[p.R].p0 == p.req[0].p0) base = p.q;            // no prefix at all: a map that nothing is read by
+  const int tokens = p.req[p.R].p0;                        // (some request has a prefix, or no unit would be there)
   // a dimension of one entry may come with any stride: it is never multiplied
   const int64_t hs = p.d.n_kv_head > 1 ? p.d.prefix_head : row, ts = tokens > 1 ? p.d.prefix_token : row;
   cuuint64_t gdim[3] = {(cuuint64_t)row, (cuuint64_t)p.d.n_kv_head, (cuuint64_t)tokens};
