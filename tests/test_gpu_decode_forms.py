@@ -2,7 +2,7 @@
     merge    a prefix kernel (tensor cores in bf16, tiled in fp32) leaves partial results, which the kernel of the own
              keys merges: a workspace
     direct   the tensor-core kernel writes the results itself (at most one own key): none, but the same call with
-             room for two own keys has one
+             room for two own keys has one (over a few dozen keys that call may have none either: not told from the next)
     own      the kernel of the own keys reads the prefixes as well: none
 Tolerances are those of test_gpu_decode.py, from the same arithmetic; the reference runs in 64 bits on the GPU.
 """
@@ -260,3 +260,19 @@ def test_form_request_alone_and_beside_others(api, case):
     agrees(part, want)
     for a, b, tol in zip(one, part, want[2:]):
         assert bool(((a.double() - b.double()).abs() <= 2 * tol).all())
+
+
+# Shapes on both sides of the choice between the prefix kernel and the one launch of the own keys' kernel.
+CHOICE = [([300] * 16, 16, 8, 128, 23, "bf16", {2: "own", 16: "own", 64: "merge"}), ([4] * 4, 8, 8, 128, 40, "bf16", {2: "own", 128: "own", 4096: "merge"}),
+          ([459] * 5, 16, 2, 96, 2, "bf16", {2: "own", 8: "own", 64: "merge"}), ([77] * 24, 32, 8, 128, 0, "f32", {2: "own", 16: "own", 256: "merge"}),
+          ([4], 8, 8, 64, 4, "bf16", {2: "own", 200: "own", 4096: "merge"}), ([4096] * 16, 8, 8, 16, 1, "bf16", {128: "direct"})]
+
+
+@pytest.mark.parametrize("case", CHOICE, ids=lambda c: f"{c[5]}-{c[0][0]}x{len(c[0])}-{c[1]}x{c[2]}x{c[3]}-s{c[4]}")
+def test_form_chosen(api, case):
+    counts, H, H_kv, d, S, dtype, want = case
+    n, so = sum(counts), [sum(counts[:r]) for r in range(len(counts) + 1)]
+    for prefix, form in want.items():
+        x = {"q": torch.empty(n, 1, H, d, dtype=DT[dtype], device="meta"), "k": torch.empty(1, H_kv, d, dtype=DT[dtype], device="meta"),
+             "ks": torch.empty(n, S, H_kv, d, device="meta") if S else None, "so": so, "po": [prefix * r for r in range(len(so))]}
+        assert form_of(api, x, False) == form, prefix
