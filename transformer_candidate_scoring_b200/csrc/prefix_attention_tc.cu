@@ -34,7 +34,8 @@
 // behind a prefix are kept out twice: their scores are replaced by -inf, and the V rows that the
 // last 16-key slice would still multiply by 0 are zeroed in shared memory (0 x NaN is NaN).
 //
-// Every wait is bounded: a stalled barrier sets an error bit and the kernel unwinds.
+// Every wait is bounded: a stalled barrier sets an error bit and the kernel unwinds, behind its copies and products
+// in flight.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -146,6 +147,7 @@ struct Bars {
   uint32_t qfull, sfull, pfull, odone;     // per tile (pfull: two per tile; qfull: per buffer if there are two)
   uint32_t qempty;                         // per buffer
   uint32_t ml_full, ml_empty;
+  uint32_t drain;                          // unwinding: the products issued so far
 };
 
 // One thread: streams the K (or V) steps of every unit into its ring.
@@ -271,6 +273,11 @@ __device__ void issue_mmas(const TcParams& p, uint32_t tmem, uint32_t smem, cons
       if (i + 2 < n_jobs) qk(i + 2);
     }
     buf ^= 1;
+  }
+  if (!ok) {   // unwinding: products in flight end before tensor and shared memory are given back
+    int none = 0;
+    if (elect_one()) mma_commit(b.drain);
+    mbar_wait_idle(b.drain, 0, &none, 200000000ull);
   }
 }
 
@@ -659,11 +666,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   auto take = [&](int n) { const uint32_t r = at; at += 8 * n; return r; };
   b.kfull = take(L::NK); b.kempty = take(L::NK); b.vfull = take(L::NV); b.vempty = take(L::NV);
   b.qfull = take(2); b.sfull = take(2); b.pfull = take(4); b.odone = take(2);
-  b.ml_full = take(1); b.ml_empty = take(1); b.qempty = take(2);
+  b.ml_full = take(1); b.ml_empty = take(1); b.qempty = take(2); b.drain = take(1);
   constexpr bool kAhead = kQAhead<DH, kOne>;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::BAR + 248);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::BAR + 252);
-  static_assert((2 * L::NK + 2 * L::NV + 14) * 8 <= 248, "barriers");
+  static_assert((2 * L::NK + 2 * L::NV + 15) * 8 <= 248, "barriers");
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < L::NK; ++i) { mbar_init(b.kfull + 8 * i, 1); mbar_init(b.kempty + 8 * i, 1); }
@@ -678,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     }
     mbar_init(b.ml_full, 128);
     mbar_init(b.ml_empty, 128);
+    mbar_init(b.drain, 1);
     mbar_fence_init();
   }
   if (warp == 11) {
