@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_decode import DT, api, attn_inputs, call, check_select, dev, ok, select_reference  # noqa: F401  (api: a fixture)
+from test_gpu_decode import DT, api, attn_inputs, bits, call, check_select, dev, ok, select_reference  # noqa: F401  (api: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -100,6 +100,48 @@ def test_select_largest_sizes(api, W, V, k, dtype):
         found += [(float(cum[0, b]) + float(y[v] - lse), b, float(y[v]), int(v)) for v in at[torch.argsort(-y[at], stable=True)[:k + 50]]]
     found.sort(key=lambda c: (-c[0], c[1], -c[2], c[3]))
     check_select(got, [found], k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W,V,k", [(32, 8192, 32), (32, 131072, 256), (1, 100003, 7), (256, 2500, 256)])
+@pytest.mark.parametrize("fill", [0.0, -1e9])
+def test_select_level_rows(api, fill, W, V, k, dtype):
+    """Beams of equal logits: the lowest tokens of the first of the best beams, in each of two requests."""
+    x = torch.full((2 * W, V), fill, device="cuda").to(DT[dtype])
+    cum = torch.full((2, W), -1.0)
+    cum[1, :W // 2] = -1.5
+    got = api.beam_select(x, cum.cuda(), k)
+    ok(api)
+    for r, b in ((0, 0), (1, W // 2)):
+        assert got[0][r].tolist() == [b] * k and got[1][r].tolist() == list(range(k))
+    assert (got[2].double().cpu() - (-1.0 - math.log(V))).abs().max() <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [5000, 60000])
+@pytest.mark.parametrize("n1,n3,n4", [(100, 50, 1600), (256, 0, 1600), (0, 300, 1600), (255, 1, 1600), (7, 2, 1700)])
+def test_select_ties_across_beams(api, n1, n3, n4, V, dtype):
+    """Beams with copies of one row of three values, three of them with equal totals, whose masks allow few of
+    its best tokens: more tokens tie at the last place than are sorted, and the ties go on from beam to beam."""
+    W, k, best = 6, 256, [1, 3, 4]
+    g = torch.Generator().manual_seed(V + n1)
+    row = torch.randint(0, 3, (V,), generator=g).float()
+    row[torch.randperm(V, generator=g)[:1800]] = 2.0
+    top = torch.nonzero(row == 2).view(-1)
+    allowed = torch.zeros(W, V, dtype=torch.bool)
+    want = []
+    for b, n in zip(best, (n1, n3, n4)):
+        at = top[torch.randperm(len(top), generator=g)[:n]].sort().values
+        allowed[b, at] = True
+        allowed[b, torch.nonzero(row == 0).view(-1)] = True
+        want += [(b, int(v)) for v in at]
+    allowed[[0, 2, 5]] = True
+    cum = torch.tensor([[-9.0, -1.0, -9.0, -1.0, -1.0, -9.0]])
+    x = row.expand(W, V).contiguous().to(DT[dtype])
+    got = api.beam_select(x.cuda(), cum.cuda(), k, allowed=bits(allowed).cuda())
+    ok(api)
+    assert list(zip(got[0][0].tolist(), got[1][0].tolist())) == want[:k]
+    assert (got[2][0] == got[2][0, 0]).all()
 
 
 def test_select_nothing_to_offer(api):

@@ -15,8 +15,11 @@
 // 64 x 16 rows of 131072 bf16: the sums 48 us (5.6 TB/s, the exponentials' unit 70 % busy), the choice 13 us,
 // a chain of some ten barriers that few threads have work between.  Lists of the best per chunk of a row
 // took 87 us for the first part, rings filled by cp.async under a persistent grid 108.
-// When more tokens reach the bound than the sort holds (long runs of equal logits), the exact k-th
-// candidate is found by bisection over the tokens themselves.
+// When more tokens reach the bound than the sort holds (long runs of equal logits: beams that have nothing to tell
+// their tokens apart, rows filled with a mask's value), the exact k-th candidate is found by bisection over
+// the tokens themselves: over the range of their totals, then, among equal ones, in the beam that it falls into.
+// 32 beams of 8192 (131072) equal logits: 0.6 ms (9.5), where bisections over all values of a total and of a tie
+// took 13.6 (214).
 //
 // Which lane sums which token depends on the token alone, not on the row's address, so equal
 // rows get equal sums and ties between their beams stay ties.
@@ -24,6 +27,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "model.cuh"
 
@@ -341,6 +345,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   __shared__ uint32_t s_key[kPickCap], s_best[kPickThreads], s_cut;
   __shared__ __align__(16) uint32_t s_sel_key[kPickCap];
   __shared__ float s_up[kPickGroups];
+  __shared__ unsigned long long s_range[2];
   __shared__ int s_count, s_tiles, s_groups, s_tile[kPickTiles], s_group[kPickGroups];
   extern __shared__ Rank s_rank[];                // [kPickCap]
   int* s_sel = reinterpret_cast<int*>(s_rank + kPickCap);
@@ -539,9 +544,14 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   }
   const int n_scan = (noted ? s_groups : n_group) * kVecs;
   // f(beam, logit, token) for every token of those groups that may reach the bound, a vector at a time; a
-  // finished beam gives its pad token
-  auto each = [&](auto f) {
-    for (int j = tid; j < n_scan; j += kPickThreads) {
+  // finished beam gives its pad token.  With `again`, of one beam alone where `only` names it: few calls come to this, and
+  // its code is kept small (the vectors unrolled here too: 7 x 50 rows of 50257 fp32 29 us instead of 28).
+  int only = -1;
+  auto each = [&](auto again, auto f) {
+    constexpr bool kAgain = decltype(again)::value;
+    const bool part = kAgain && !noted && only >= 0;
+    const int last = part ? (only + 1) * per_row * kVecs : n_scan;
+    for (int j = (part ? only * per_row * kVecs : 0) + tid; j < last; j += kPickThreads) {
       int b, i;
       if (noted) {
         if (s_up[j / kVecs] < bound) continue;
@@ -551,6 +561,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
         b = j / kVecs / per_row;
         i = j / kVecs % per_row;
       }
+      if (kAgain && only >= 0 && b != only) continue;
       const int kind = s_kind[b];
       if (kind == 2 && i == 0 && j % kVecs == 0) f(b, 0.f, p.pad_token);
       if (kind != 1) continue;
@@ -561,7 +572,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
       const uint32_t bits = p.allowed ? allowed_bits(p, row0 + b, v) : ~0u;
       const float above = s_max[b] == INFINITY ? FLT_MAX : -INFINITY;    // beside +inf, the others' totals are -inf
-#pragma unroll
+#pragma unroll(kAgain ? 1 : N)
       for (int e = 0; e < N; ++e) {
         const float x = P::at(w[e / (N / 4)], e);
         if (x > above && (bits >> e & 1u)) {
@@ -574,7 +585,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
   auto rank_of = [&](int b, float x, int token) {
     return Rank{s_kind[b] == 2 ? okey(s_cum[b]) : key_of(b, x), tie_of(b, x, token)};
   };
-  each([&](int b, float x, int token) {
+  each(std::false_type(), [&](int b, float x, int token) {
     const int at = atomicAdd(&s_count, 1);
     if (at < kPickCap) s_rank[at] = Rank{(unsigned long long)__float_as_uint(x), tie_of(b, x, token)};
   });
@@ -587,35 +598,88 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     }
     __syncthreads();
   } else {
-    // too many: the exact k-th candidate, by its total and then by its tie
-    auto count_if = [&](auto pred) {
-      int c = 0;
-      each([&](int b, float x, int token) { c += pred(rank_of(b, x, token)); });
+    // too many: the exact k-th candidate, by its total and then by its tie.  One scan of the tokens per turn:
+    // the range of their totals, counts at probes into it, the beams of those equal to the k-th, the range of the
+    // ties in the beam that the last of them is from, counts at probes, and what is to be taken.
+    enum { kTotals, kTotalCount, kBeams, kTies, kTieCount, kTake };
+    unsigned long long a = 0, b = 0, kth = 0, probe = 0;
+    int want = k;
+    for (int turn = kTotals;;) {
       __syncthreads();
-      if (tid == 0) s_count = 0;
+      if (tid == 0) {
+        s_count = 0;
+        s_range[0] = ~0ull;
+        s_range[1] = 0ull;
+      }
+      if (turn == kBeams && tid < TR_MAX_BEAMS) s_key[tid] = 0u;
       __syncthreads();
+      unsigned long long lo64 = ~0ull, hi64 = 0ull;
+      int c = 0, run = 0, run_beam = 0;                    // (tokens of one beam counted before they are added)
+      each(std::true_type(), [&](int beam, float x, int token) {
+        const Rank q = rank_of(beam, x, token);
+        if (turn == kTotals || turn == kTies) {
+          if (turn == kTotals ? q.key != 0ull : q.key == kth) {
+            const unsigned long long y = turn == kTotals ? q.key : q.tie;
+            lo64 = min(lo64, y);
+            hi64 = max(hi64, y);
+          }
+        } else if (turn == kTotalCount) {
+          c += q.key >= probe;
+        } else if (turn == kBeams) {
+          c += q.key > kth;
+          if (q.key == kth) {
+            if (beam != run_beam) {
+              if (run) atomicAdd(&s_key[run_beam], (uint32_t)run);
+              run = 0;
+              run_beam = beam;
+            }
+            ++run;
+          }
+        } else if (turn == kTieCount) {
+          c += q.key == kth && q.tie >= probe;
+        } else if (q.key > kth || (q.key == kth && q.tie >= a)) {
+          s_rank[atomicAdd(&s_count, 1)] = q;              // k at most (ties differ)
+        }
+      });
+      if (run) atomicAdd(&s_key[run_beam], (uint32_t)run);
+      if (lo64 <= hi64) {
+        atomicMin(&s_range[0], lo64);
+        atomicMax(&s_range[1], hi64);
+      }
       c = __reduce_add_sync(0xffffffffu, c);
       if (lane == 0 && c) atomicAdd(&s_count, c);
       __syncthreads();
-      return s_count;
-    };
-    unsigned long long a = 1, b = ~0ull;
-    while (a < b) {
-      const unsigned long long mid = a + (b - a) / 2 + 1;
-      if (count_if([&](const Rank& q) { return q.key >= mid; }) >= k) a = mid; else b = mid - 1;
+      if (turn == kTake) break;
+      if (turn == kTotals || turn == kTies) {
+        a = s_range[0];
+        b = s_range[1];
+        if (a > b) {                                       // every total is -inf
+          if (tid == 0) s_count = 0;
+          break;
+        }
+        turn = turn == kTotals ? kTotalCount : kTieCount;
+      } else if (turn != kBeams) {
+        if (s_count >= want) a = probe; else b = probe - 1;
+      } else {
+        want -= s_count;
+        int beam = 0;
+        while (beam < p.W && (int)s_key[beam] < want) want -= (int)s_key[beam++];
+        only = beam < p.W ? beam : -1;                     // (-1: all of them are taken)
+        a = 0;
+        turn = only >= 0 ? kTies : kTake;
+      }
+      if (turn == kTotalCount || turn == kTieCount) {
+        if (a < b) {
+          probe = a + (b - a) / 2 + 1;
+        } else if (turn == kTotalCount) {
+          kth = a;
+          turn = kBeams;
+        } else {
+          only = -1;
+          turn = kTake;
+        }
+      }
     }
-    unsigned long long ta = 0, tb = ~0ull;
-    while (ta < tb) {
-      const unsigned long long mid = ta + (tb - ta) / 2 + 1;
-      if (count_if([&](const Rank& q) { return q.key > a || (q.key == a && q.tie >= mid); }) >= k) ta = mid; else tb = mid - 1;
-    }
-    __syncthreads();
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    each([&](int b, float x, int token) {
-      const Rank q = rank_of(b, x, token);
-      if (q.key > a || (q.key == a && q.tie >= ta)) s_rank[atomicAdd(&s_count, 1)] = q;   // exactly k (ties differ)
-    });
     __syncthreads();
     count = s_count;
   }
