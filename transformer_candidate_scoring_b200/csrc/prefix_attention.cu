@@ -625,7 +625,7 @@ constexpr int kMmaSuffix = 8;      // own tokens from which suffix_kernel takes 
 // kernel's cost is 3 and 0.74 (fp32: 1.8) per step of the plan's, and 8 bytes per partial result; finish_kernel takes
 // 3.1 ps (fp32: 4.5) per key and lane of a row or 0.27 us per key in turn, and 5 us and 25 ps per lane beside; suffix_kernel
 // 0.6 ns (d_head up to 64: 0.4) per 16 keys of a sequence and key head.  Without and with:
-//   16 x 300 sequences, 16 heads of 128 on 8, 23 own keys, prefixes of 2, 32, 64 keys    190 and 154, 175, 221 us
+//   16 x 300 sequences, 16 heads of 128 on 8, 23 own keys, prefixes of 2, 32, 64 keys    190 and 154, 175, 221 us (the choice changes between 16 and 32)
 //   4 x 4, 8 heads of 128, 40 own keys, prefixes of 2, 64, 128                           11.5 and 4.2, 5.2, 6.1
 //   5 x 459, 16 heads of 96 on 2, two own keys, prefixes of 2, 8                         43 and 28, 34
 //   24 x 77 fp32, 32 heads of 128 on 8, none, prefixes of 2, 8, 16                       112 and 32, 49, 83

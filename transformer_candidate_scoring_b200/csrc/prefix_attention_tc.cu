@@ -20,7 +20,7 @@
 //   warp 11             tensor memory; the next unit's Q where shared memory has room for it
 //
 // A step's chain -- S, softmax, P V, of which the next S waits because P lies where S was -- bounds
-// many rows: 2 x 4,096 sequences with 16 heads of 128 on 4 over 4,096 keys take 286 us (960 TFLOP/s),
+// many rows: 2 x 4,096 sequences with 16 heads of 128 on 4 over 4,096 keys take 279 us (985 TFLOP/s),
 // the tensor core busy 45 % and the exponentials' unit 45 % of it.  Steps of 64 keys with two S buffers
 // per tile, separate S and P with steps of 80 keys, one MMA warp per tile, two threads per row and a part
 // of the exponentials on the FMA pipes measured no faster (319 to 427 us against 322 of the kernel then).
