@@ -218,6 +218,28 @@ def test_buffers_of_a_call_on_another_stream(api, what, run, handle):
     ok(api)
 
 
+@pytest.mark.parametrize("what,run", [("attention", call), ("selection", _choose)])
+def test_buffers_come_from_the_stream_given(api, what, run):
+    """A stream, its handle, the default stream's handle 0 and none at all, called while another stream is current:
+    each result is in memory that torch's allocator holds for the call's own stream."""
+    x = _stream_inputs(what, 3)
+    want = run(api, x)
+    ok(api)
+    side, here = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def owner(t):
+        seg, = [s for s in torch.cuda.memory_snapshot() if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+        return seg["stream"]
+    for stream, handle in ((side, side.cuda_stream), (side.cuda_stream, side.cuda_stream), (0, 0), (torch.cuda.default_stream(), 0),
+                           (None, here.cuda_stream)):
+        with torch.cuda.stream(here):
+            got = run(api, x, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert [owner(t) for t in got] == [handle] * len(got), stream
+    ok(api)
+
+
 # ------------------------------------------------------------------ reordering
 def test_reorder_refuses_conflicts_among_many_states(api):
     """Over 64 states: one listed twice, an out that is another's state, two equal outs, wherever they stand,

@@ -284,8 +284,9 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(raw, like.get_device())
+        raw, dev = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), like.get_device()
+        # (torch takes an external handle of 0 for a stream yet to be made)
+        stream = torch.cuda.ExternalStream(raw, dev) if raw else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
